@@ -12,6 +12,12 @@ importing works without the library but every call fails loudly until
 Layouts (see ``include/dcn.h``): x [B, H, W, Cin], offset [B, 2*G*K*K, Ho, Wo]
 (channel g*2K^2 + 2k = row offset, +1 = column offset), mask [B, G*K*K, Ho, Wo],
 weight [Cout, K, K, Cin], bias [Cout], y [B, Ho, Wo, Cout]; gradients float32.
+
+Around the layer: ``linear`` (the 1x1 convolutions before and after it, the fully
+connected layers behind RoI pooling: matrix product, bias, residual and
+activation in one kernel) and ``group_norm`` (with the activation behind it),
+both with autograd. Their activation gradients have the input's dtype, their
+parameter gradients are float32.
 """
 from __future__ import annotations
 
@@ -25,7 +31,8 @@ import torch
 __all__ = [
     "forward", "forward_noalloc", "backward_data", "backward_input", "backward_offset_mask", "backward_weight", "output_size",
     "workspace_size", "forward_path", "check_status", "launch_count", "library_path", "DeformConv2dFunction",
-    "deform_conv2d", "DcnError",
+    "deform_conv2d", "DcnError", "linear", "linear_forward", "linear_backward", "LinearFunction", "group_norm",
+    "group_norm_forward", "group_norm_backward", "GroupNormFunction",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -43,7 +50,8 @@ DCN_F32, DCN_BF16 = 0, 1
 DCN_FLAG_GENERIC = 0x1
 DCN_FLAG_NO_TF32 = 0x2
 DCN_ERR_TIMEOUT, DCN_ERR_RANGE = -4, -6
-OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT = 0, 1, 2
+OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BACKWARD = 0, 1, 2, 3
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 _DTYPES = {torch.float32: DCN_F32, torch.bfloat16: DCN_BF16}
 
 
@@ -61,6 +69,15 @@ class Params(ctypes.Structure):
 class RoiParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "W", "C", "R", "k")] + [
         ("gamma", ctypes.c_float), ("dtype", ctypes.c_int), ("flags", ctypes.c_uint)]
+
+
+class LinearParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("M", "N", "K", "act", "dtype")] + [("flags", ctypes.c_uint)]
+
+
+class NormParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "W", "C", "groups")] + [
+        ("eps", ctypes.c_float), ("act", ctypes.c_int), ("dtype", ctypes.c_int), ("flags", ctypes.c_uint)]
 
 
 def library_path() -> str:
@@ -94,6 +111,15 @@ def _load():
         RP = ctypes.POINTER(RoiParams)
         lib.dcn_droi_pool_forward.argtypes = [RP, vp, vp, vp, vp, vp, vp]
         lib.dcn_droi_pool_backward.argtypes = [RP, vp, vp, vp, vp, vp, fp, fp, fp, vp]
+        LP, NP = ctypes.POINTER(LinearParams), ctypes.POINTER(NormParams)
+        for fn in (lib.dcn_linear_workspace_size, lib.dcn_group_norm_workspace_size):
+            fn.restype = sz
+        lib.dcn_linear_workspace_size.argtypes = [LP, ctypes.c_int]
+        lib.dcn_linear_forward.argtypes = [LP, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.dcn_linear_backward.argtypes = [LP, vp, vp, vp, vp, vp, fp, fp, vp, vp, sz, vp]
+        lib.dcn_group_norm_workspace_size.argtypes = [NP, ctypes.c_int]
+        lib.dcn_group_norm_forward.argtypes = [NP, vp, vp, vp, vp, fp, vp, sz, vp]
+        lib.dcn_group_norm_backward.argtypes = [NP, vp, vp, vp, fp, vp, vp, fp, fp, vp, sz, vp]
         lib.dcn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, vp]
         lib.dcn_last_error_string.restype = ctypes.c_char_p
         lib.dcn_check_status.argtypes = [vp]
@@ -312,6 +338,147 @@ def droi_pool_backward(x, rois, offset, mask, grad_y, k, gamma=1.0, *, need_offs
     return gx, goff, gm
 
 
+def _activation(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
+    return ACTIVATIONS[activation]
+
+
+def _check_shape(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _scratch(n, device, workspace):
+    """(tensor, bytes) of a workspace of at least n bytes: the caller's, or a new one."""
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
+
+
+def _linear_params(x, weight, activation, generic):
+    """(params, shape of y) for x [..., K] and weight [N, K] or [N, 1, 1, K]."""
+    if x.dim() < 1 or weight.dim() not in (2, 4) or weight.dim() == 4 and tuple(weight.shape[1:3]) != (1, 1):
+        raise ValueError("x must be [..., K] and weight [N, K] or [N, 1, 1, K]")
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
+    N, K = weight.shape[0], weight.shape[-1]
+    if x.shape[-1] != K:
+        raise ValueError("x must be [..., %d] for weight %s, got %s" % (K, tuple(weight.shape), tuple(x.shape)))
+    if N < 1 or K < 1:
+        raise ValueError("weight must not be empty, got %s" % (tuple(weight.shape),))
+    p = LinearParams(x.numel() // K, N, K, _activation(activation), _DTYPES[x.dtype],
+                     DCN_FLAG_GENERIC if generic else 0)
+    return p, (*x.shape[:-1], N)
+
+
+def linear_workspace_size(p: LinearParams, op: int) -> int:
+    return int(_load().dcn_linear_workspace_size(ctypes.byref(p), op))
+
+
+def linear_forward(x, weight, bias=None, residual=None, activation="none", *, need_preact=False, out=None,
+                   workspace=None, generic=False):
+    """y [..., N] = act(x W^T + bias + residual) for x [..., K] (any leading dimensions: the pixels of an NHWC
+    map, or rows) and weight [N, K] or [N, 1, 1, K]; bias [N], residual [..., N] or None; activation "none",
+    "relu", "silu" or "gelu" (with erf). need_preact: (y, z) with the pre-activation z, which the backward pass
+    of silu and gelu takes. out: y to write; it may be the residual."""
+    lib = _load()
+    p, shape = _linear_params(x, weight, activation, generic)
+    _check_tensors(x.dtype, x.device, x=x, weight=weight, bias=bias, residual=residual, out=out)
+    _check_shape("bias", bias, (p.N,))
+    _check_shape("residual", residual, shape)
+    _check_shape("out", out, shape)
+    with torch.cuda.device(x.device):
+        y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
+        z = torch.empty(shape, dtype=x.dtype, device=x.device) if need_preact else None
+        ws, nws = _scratch(linear_workspace_size(p, OP_FORWARD), x.device, workspace)
+        _check(lib.dcn_linear_forward(ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y),
+                                      _ptr(z), _ptr(ws), nws, _stream(x.device)))
+    return (y, z) if need_preact else y
+
+
+def linear_backward(x, weight, saved, grad_y, activation="none", *, need_input=True, need_weight=True, need_bias=True,
+                    need_residual=False, workspace=None, generic=False):
+    """(grad_x, grad_weight, grad_bias, grad_residual) of linear_forward, entries not requested None. saved: what
+    the forward left, y for relu, the pre-activation z for silu and gelu, None for none. grad_x and
+    grad_residual have x's dtype, grad_weight (weight's shape) and grad_bias are float32."""
+    lib = _load()
+    p, shape = _linear_params(x, weight, activation, generic)
+    if (saved is None) != (activation == "none"):
+        raise ValueError("saved must be %s for activation %r" % (
+            "None" if activation == "none" else "the output" if activation == "relu" else "the pre-activation",
+            activation))
+    _check_tensors(x.dtype, x.device, x=x, weight=weight, saved=saved, grad_y=grad_y)
+    _check_shape("saved", saved, shape)
+    _check_shape("grad_y", grad_y, shape)
+    with torch.cuda.device(x.device):
+        f32 = dict(dtype=torch.float32, device=x.device)
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_input else None
+        gw = torch.empty(weight.shape, **f32) if need_weight else None
+        gb = torch.empty((p.N,), **f32) if need_bias else None
+        gr = torch.empty(shape, dtype=x.dtype, device=x.device) if need_residual else None
+        ws, nws = _scratch(linear_workspace_size(p, OP_BACKWARD), x.device, workspace)
+        _check(lib.dcn_linear_backward(ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(saved), _ptr(grad_y), _ptr(gx),
+                                       _ptr(gw), _ptr(gb), _ptr(gr), _ptr(ws), nws, _stream(x.device)))
+    return gx, gw, gb, gr
+
+
+def _norm_params(x, groups, eps, activation):
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, W, C]")
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
+    B, H, W, C = x.shape
+    return NormParams(B, H, W, C, int(groups), float(eps), _activation(activation), _DTYPES[x.dtype], 0)
+
+
+def group_norm_workspace_size(p: NormParams, op: int) -> int:
+    return int(_load().dcn_group_norm_workspace_size(ctypes.byref(p), op))
+
+
+def group_norm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", *, out=None, workspace=None):
+    """(y, stats): y = act(gamma (x - mean) rstd + beta) of x [B, H, W, C] over each sample's groups of
+    C / groups neighbouring channels, stats float32 [B, groups, 2] = (mean, rstd). gamma, beta [C] or None;
+    activation as for linear_forward. out: y to write; it may be x."""
+    lib = _load()
+    p = _norm_params(x, groups, eps, activation)
+    _check_tensors(x.dtype, x.device, x=x, gamma=gamma, beta=beta, out=out)
+    _check_shape("gamma", gamma, (p.C,))
+    _check_shape("beta", beta, (p.C,))
+    _check_shape("out", out, x.shape)
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        stats = torch.empty((p.B, max(p.groups, 0), 2), dtype=torch.float32, device=x.device)
+        ws, nws = _scratch(group_norm_workspace_size(p, OP_FORWARD), x.device, workspace)
+        _check(lib.dcn_group_norm_forward(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats),
+                                          _ptr(ws), nws, _stream(x.device)))
+    return y, stats
+
+
+def group_norm_backward(x, gamma, beta, stats, grad_y, groups, activation="none", *, need_input=True,
+                        need_params=True, workspace=None):
+    """(grad_x, grad_gamma, grad_beta) of group_norm_forward, given its x and stats: grad_x in x's dtype,
+    grad_gamma and grad_beta [C] float32, None where gamma or beta is None or not requested."""
+    lib = _load()
+    p = _norm_params(x, groups, 1.0, activation)
+    _check_tensors(x.dtype, x.device, x=x, gamma=gamma, beta=beta, grad_y=grad_y)
+    _check_tensors(torch.float32, x.device, stats=stats)
+    _check_shape("gamma", gamma, (p.C,))
+    _check_shape("beta", beta, (p.C,))
+    _check_shape("stats", stats, (p.B, p.groups, 2))
+    _check_shape("grad_y", grad_y, x.shape)
+    with torch.cuda.device(x.device):
+        f32 = dict(dtype=torch.float32, device=x.device)
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_input else None
+        gg = torch.empty((p.C,), **f32) if need_params and gamma is not None else None
+        gb = torch.empty((p.C,), **f32) if need_params and beta is not None else None
+        ws, nws = _scratch(group_norm_workspace_size(p, OP_BACKWARD), x.device, workspace)
+        _check(lib.dcn_group_norm_backward(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(stats),
+                                           _ptr(grad_y), _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws), nws,
+                                           _stream(x.device)))
+    return gx, gg, gb
+
+
 def backward_data(x, offset, mask, weight, grad_y, stride=1, padding=0, dilation=1, *, need_input=True,
                   need_offset=True, need_mask=True, workspace=None, generic=False, out=None):
     """(grad_x, grad_offset, grad_mask) in one pass; entries not requested are None."""
@@ -399,3 +566,62 @@ class DeformConv2dFunction(torch.autograd.Function):
 def deform_conv2d(x, offset, weight, bias=None, stride=1, padding=0, dilation=1, mask=None):
     """Differentiable DCNv2 on NHWC x; argument order as torchvision's deform_conv2d."""
     return DeformConv2dFunction.apply(x, offset, mask, weight, bias, stride, padding, dilation)
+
+
+class LinearFunction(torch.autograd.Function):
+    """Autograd wrapper over linear_forward and linear_backward. Parameter gradients are float32 and are cast to
+    each parameter's dtype on return."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        keep_z = activation in ("silu", "gelu") and any(ctx.needs_input_grad)
+        y = linear_forward(x, weight, bias, residual, activation, need_preact=keep_z)
+        y, saved = y if keep_z else (y, y if activation == "relu" else None)
+        ctx.save_for_backward(x, weight, saved)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        x, weight, saved = ctx.saved_tensors
+        nx, nw, nb, nr, _ = ctx.needs_input_grad
+        gy = grad_y.to(x.dtype).contiguous()
+        gx, gw, gb, gr = linear_backward(x, weight, saved, gy, ctx.activation, need_input=nx, need_weight=nw,
+                                         need_bias=nb, need_residual=nr and ctx.activation != "none")
+        if nr and ctx.activation == "none":
+            gr = gy
+        cast = lambda g: None if g is None else g.to(weight.dtype)
+        return gx, cast(gw), cast(gb), gr, None
+
+
+def linear(x, weight, bias=None, residual=None, activation="none"):
+    """Differentiable act(x W^T + bias + residual); shapes as for linear_forward."""
+    return LinearFunction.apply(x, weight, bias, residual, activation)
+
+
+class GroupNormFunction(torch.autograd.Function):
+    """Autograd wrapper over group_norm_forward and group_norm_backward. Parameter gradients are float32 and are
+    cast to each parameter's dtype on return."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, groups, eps, activation):
+        y, stats = group_norm_forward(x, gamma, beta, groups, eps, activation)
+        ctx.save_for_backward(x, gamma, beta, stats)
+        ctx.conf = (groups, activation)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_y):
+        x, gamma, beta, stats = ctx.saved_tensors
+        groups, activation = ctx.conf
+        nx, ng, nb = ctx.needs_input_grad[:3]
+        gx, gg, gb = group_norm_backward(x, gamma, beta, stats, grad_y.to(x.dtype).contiguous(), groups, activation,
+                                         need_input=nx, need_params=ng or nb)
+        return (gx, gg.to(x.dtype) if ng else None, gb.to(x.dtype) if nb else None, None, None, None)
+
+
+def group_norm(x, gamma, beta, groups, eps=1e-5, activation="none"):
+    """Differentiable act(GroupNorm(x)) on NHWC x; shapes as for group_norm_forward."""
+    return GroupNormFunction.apply(x, gamma, beta, groups, eps, activation)

@@ -556,6 +556,172 @@ int dcn_droi_pool_backward(const dcn_roi_params_t* params, const void* x, const 
     return ok();
 }
 
+// ------------------------------------------------------------ linear layer --
+
+static int linear_shape(const dcn_linear_params_t* p, dcn::LinearShape& s) {
+    if (!p) return fail(DCN_ERR_INVALID_ARG, "params is NULL");
+    if (p->M < 0 || p->N < 1 || p->K < 1)
+        return fail(DCN_ERR_INVALID_ARG, "need M >= 0, N >= 1, K >= 1 (M=%d N=%d K=%d)", p->M, p->N, p->K);
+    if (p->act < DCN_ACT_NONE || p->act > DCN_ACT_GELU)
+        return fail(DCN_ERR_INVALID_ARG, "unknown activation %d", p->act);
+    if (p->dtype != DCN_F32 && p->dtype != DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "unknown dtype %d", p->dtype);
+    if ((long long)p->M * p->K > kMaxElems || (long long)p->M * p->N > kMaxElems || (long long)p->N * p->K > kMaxElems)
+        return fail(DCN_ERR_UNSUPPORTED, "a tensor exceeds 2^31-1 elements");
+    s.M = p->M;
+    s.N = p->N;
+    s.K = p->K;
+    s.act = p->act;
+    return DCN_OK;
+}
+
+size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op) {
+    dcn::LinearShape s;
+    std::string keep = g_err;
+    if (linear_shape(params, s) != DCN_OK) {
+        g_err = keep;
+        return 0;
+    }
+    (void)op;
+    return 0;
+}
+
+int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const void* weight, const void* bias,
+                       const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes, void* stream) {
+    DCN_TRACE("dcn_linear_forward");
+    dcn::LinearShape s;
+    TRY(linear_shape(params, s));
+    const size_t es = elem_size(params->dtype);
+    const bool any = s.M > 0;
+    TRY(check_ptr(x, "x", es, any));
+    TRY(check_ptr(weight, "weight", es, true));
+    TRY(check_ptr(bias, "bias", es, false));
+    TRY(check_ptr(residual, "residual", es, false));
+    TRY(check_ptr(y, "y", es, any));
+    TRY(check_ptr(z, "z", es, false));
+    if (!any) return ok();
+    (void)workspace, (void)workspace_bytes;
+    int n = 0;
+    cudaError_t e = dcn::linear_forward(s, params->dtype == DCN_BF16, x, weight, bias, residual, y, z,
+                                        (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return cuda_fail(e, "linear forward launch");
+    return ok();
+}
+
+int dcn_linear_backward(const dcn_linear_params_t* params, const void* x, const void* weight, const void* saved,
+                        const void* grad_y, void* grad_x, float* grad_weight, float* grad_bias, void* grad_residual,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    DCN_TRACE("dcn_linear_backward");
+    dcn::LinearShape s;
+    TRY(linear_shape(params, s));
+    const size_t es = elem_size(params->dtype);
+    const bool any = s.M > 0;
+    TRY(check_ptr(x, "x", es, any && grad_weight));
+    TRY(check_ptr(weight, "weight", es, any && grad_x));
+    TRY(check_ptr(saved, "saved", es, any && s.act != DCN_ACT_NONE));
+    TRY(check_ptr(grad_y, "grad_y", es, any));
+    TRY(check_ptr(grad_x, "grad_x", es, false));
+    TRY(check_ptr(grad_weight, "grad_weight", 4, false));
+    TRY(check_ptr(grad_bias, "grad_bias", 4, false));
+    TRY(check_ptr(grad_residual, "grad_residual", es, false));
+    (void)workspace, (void)workspace_bytes;
+    if (!any) grad_x = grad_residual = nullptr;  // no rows; grad_weight and grad_bias are zero
+    int n = 0;
+    cudaError_t e = dcn::linear_backward(s, params->dtype == DCN_BF16, x, weight, saved, grad_y, grad_x, grad_weight,
+                                         grad_bias, grad_residual, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return cuda_fail(e, "linear backward launch");
+    return ok();
+}
+
+// ------------------------------------------------------ group normalisation --
+
+static int norm_shape(const dcn_norm_params_t* p, dcn::NormShape& s) {
+    if (!p) return fail(DCN_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 1 || p->H < 1 || p->W < 1 || p->C < 1 || p->groups < 1)
+        return fail(DCN_ERR_INVALID_ARG, "need B, H, W, C, groups >= 1 (B=%d H=%d W=%d C=%d groups=%d)", p->B, p->H,
+                    p->W, p->C, p->groups);
+    if (p->C % p->groups)
+        return fail(DCN_ERR_INVALID_ARG, "C=%d is not a multiple of groups=%d", p->C, p->groups);
+    if (!(p->eps > 0.f && p->eps < 3.0e38f)) return fail(DCN_ERR_INVALID_ARG, "eps must be positive and finite");
+    if (p->act < DCN_ACT_NONE || p->act > DCN_ACT_GELU)
+        return fail(DCN_ERR_INVALID_ARG, "unknown activation %d", p->act);
+    if (p->dtype != DCN_F32 && p->dtype != DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "unknown dtype %d", p->dtype);
+    if ((double)p->B * p->H * p->W * p->C > (double)kMaxElems)
+        return fail(DCN_ERR_UNSUPPORTED, "a tensor exceeds 2^31-1 elements");
+    s.B = p->B;
+    s.HW = p->H * p->W;
+    s.C = p->C;
+    s.groups = p->groups;
+    s.act = p->act;
+    s.eps = p->eps;
+    return DCN_OK;
+}
+
+size_t dcn_group_norm_workspace_size(const dcn_norm_params_t* params, int op) {
+    dcn::NormShape s;
+    std::string keep = g_err;
+    if (norm_shape(params, s) != DCN_OK) {
+        g_err = keep;
+        return 0;
+    }
+    return dcn::norm_workspace(s, params->dtype == DCN_BF16, op == DCN_OP_BACKWARD);
+}
+
+static int norm_workspace_ok(const dcn_norm_params_t* params, int op, const void* workspace, size_t bytes) {
+    const size_t need = dcn_group_norm_workspace_size(params, op);
+    if (need > 0 && (!workspace || bytes < need))
+        return fail(DCN_ERR_WORKSPACE, "group norm needs %zu bytes of workspace, got %zu", need,
+                    workspace ? bytes : (size_t)0);
+    return check_ptr(workspace, "workspace", 16, need > 0);
+}
+
+int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const void* gamma, const void* beta, void* y,
+                           float* stats, void* workspace, size_t workspace_bytes, void* stream) {
+    DCN_TRACE("dcn_group_norm_forward");
+    dcn::NormShape s;
+    TRY(norm_shape(params, s));
+    const size_t es = elem_size(params->dtype);
+    TRY(check_ptr(x, "x", es, true));
+    TRY(check_ptr(gamma, "gamma", es, false));
+    TRY(check_ptr(beta, "beta", es, false));
+    TRY(check_ptr(y, "y", es, true));
+    TRY(check_ptr(stats, "stats", 4, false));
+    TRY(norm_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+    int n = 0;
+    cudaError_t e = dcn::norm_forward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(y), x, gamma, beta, y,
+                                      stats, workspace, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return cuda_fail(e, "group norm forward launch");
+    return ok();
+}
+
+int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, const void* gamma, const void* beta,
+                            const float* stats, const void* grad_y, void* grad_x, float* grad_gamma, float* grad_beta,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    DCN_TRACE("dcn_group_norm_backward");
+    dcn::NormShape s;
+    TRY(norm_shape(params, s));
+    const size_t es = elem_size(params->dtype);
+    TRY(check_ptr(x, "x", es, true));
+    TRY(check_ptr(gamma, "gamma", es, false));
+    TRY(check_ptr(beta, "beta", es, false));
+    TRY(check_ptr(stats, "stats", 4, true));
+    TRY(check_ptr(grad_y, "grad_y", es, true));
+    TRY(check_ptr(grad_x, "grad_x", es, false));
+    TRY(check_ptr(grad_gamma, "grad_gamma", 4, false));
+    TRY(check_ptr(grad_beta, "grad_beta", 4, false));
+    if (!grad_x && !grad_gamma && !grad_beta) return ok();
+    TRY(norm_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+    int n = 0;
+    cudaError_t e = dcn::norm_backward(s, params->dtype == DCN_BF16,
+                                       aligned16(x) && aligned16(grad_y) && aligned16(grad_x), x, gamma, beta, stats,
+                                       grad_y, grad_x, grad_gamma, grad_beta, workspace, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return cuda_fail(e, "group norm backward launch");
+    return ok();
+}
+
 const char* dcn_last_error_string(void) { return g_err.c_str(); }
 
 int dcn_check_status(void* stream) {

@@ -115,6 +115,28 @@ bool bwd_gx_supported(const Shape& s);
 cudaError_t bwd_gx_tc(const Shape& s, const void* gy, const void* wt, const void* rec, int ppad, float* gx,
                       unsigned* status, cudaStream_t st, int* launches);
 
+// linear.cu — linear layer with bias, residual and activation, CUDA cores, every size and alignment.
+struct LinearShape {
+    int M, N, K, act;
+};
+cudaError_t linear_forward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* bias,
+                           const void* residual, void* y, void* z, cudaStream_t st, int* launches);
+cudaError_t linear_backward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* saved,
+                            const void* gy, void* gx, float* gw, float* gb, void* gr, cudaStream_t st, int* launches);
+
+// group_norm.cu — group normalisation with an activation, channels last. vec: x, y, grad_y and
+// grad_x are 16-byte aligned.
+struct NormShape {
+    int B, HW, C, groups, act;
+    float eps;
+};
+size_t norm_workspace(const NormShape& s, int dtype_bf16, bool backward);
+cudaError_t norm_forward(const NormShape& s, int dtype_bf16, bool vec, const void* x, const void* gamma,
+                         const void* beta, void* y, float* stats, void* ws, cudaStream_t st, int* launches);
+cudaError_t norm_backward(const NormShape& s, int dtype_bf16, bool vec, const void* x, const void* gamma,
+                          const void* beta, const float* stats, const void* gy, void* gx, float* gg, float* gb,
+                          void* ws, cudaStream_t st, int* launches);
+
 // selftest.cu — a kernel whose bounded wait can only give up (failure-detection test).
 cudaError_t selftest_wait_timeout(long long limit_cycles, cudaStream_t st);
 

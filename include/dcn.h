@@ -241,6 +241,89 @@ DCN_API int dcn_droi_pool_backward(const dcn_roi_params_t* params, const void* x
                                    const void* offset, const void* mask, const void* grad_y, float* grad_x,
                                    float* grad_offset, float* grad_mask, void* stream);
 
+/* Activations of the calls below. gelu is x/2 (1 + erf(x / sqrt 2)). */
+typedef enum {
+    DCN_ACT_NONE = 0,
+    DCN_ACT_RELU = 1,
+    DCN_ACT_SILU = 2,
+    DCN_ACT_GELU = 3
+} dcn_act_t;
+
+#define DCN_OP_BACKWARD 3 /* dcn_linear_backward, dcn_group_norm_backward */
+
+/* Linear layer: the 1x1 convolutions around a deformable layer (M pixels of an
+ * NHWC map) and the fully connected layers behind RoI pooling (M RoIs).
+ *   z = x W^T + bias + residual,  y = act(z)
+ *   x [M, K], weight [N, K], bias [N] or NULL, residual [M, N] or NULL, y [M, N]
+ * all in `dtype`. Sums, bias, residual and activation are float32; z and y are
+ * rounded once each. float32 layers keep float32 accuracy on the tensor cores
+ * (operands split in three bfloat16 terms). Infinities and NaN of a bfloat16
+ * layer spread as in the sums above; a float32 layer may turn an infinity into
+ * NaN. M may be 0. */
+typedef struct {
+    int M, N, K;
+    int act;         /* dcn_act_t */
+    int dtype;       /* DCN_F32 or DCN_BF16 */
+    unsigned flags;  /* DCN_FLAG_GENERIC or 0 */
+} dcn_linear_params_t;
+
+/* Bytes of workspace (16-byte aligned) of the forward (op DCN_OP_FORWARD) or the
+ * backward (DCN_OP_BACKWARD); 0 when none is needed or params are invalid. */
+DCN_API size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op);
+
+/* Writes y, and z [M, N] in `dtype` unless it is NULL. y and z must not overlap
+ * an input, but y may be the residual. */
+DCN_API int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const void* weight, const void* bias,
+                               const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Given grad_y [M, N] (dtype) and what the forward left in `saved` (relu: y;
+ * silu, gelu: z; none: ignored, may be NULL), with dz = grad_y act'(z):
+ *   grad_x [M, K] = dz W and grad_residual [M, N] = dz in `dtype` (they are the
+ *   next call's grad_y), grad_weight [N, K] = dz^T x and grad_bias [N] = the
+ *   column sums of dz in float32.
+ * Each output may be NULL (not computed); x may be NULL without grad_weight,
+ * weight without grad_x. relu has slope 0 at 0. Equal calls give equal bits. */
+DCN_API int dcn_linear_backward(const dcn_linear_params_t* params, const void* x, const void* weight,
+                                const void* saved, const void* grad_y, void* grad_x, float* grad_weight,
+                                float* grad_bias, void* grad_residual, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Group normalisation with an activation, channels last. Over the H*W*C/groups
+ * values of a sample's group of C/groups neighbouring channels:
+ *   mean, rstd = 1 / sqrt(variance + eps) (biased variance),
+ *   z = gamma (x - mean) rstd + beta,  y = act(z)
+ *   x, y [B, H, W, C], gamma, beta [C] or NULL (1 and 0), all in `dtype`;
+ *   stats [B, groups, 2] float32: (mean, rstd).
+ * Arithmetic is float32. A group that holds an infinity or a NaN becomes NaN;
+ * other groups do not notice. */
+typedef struct {
+    int B, H, W, C;
+    int groups;      /* C % groups == 0 */
+    float eps;       /* > 0 */
+    int act;         /* dcn_act_t */
+    int dtype;       /* DCN_F32 or DCN_BF16 */
+    unsigned flags;  /* reserved, 0 */
+} dcn_norm_params_t;
+
+/* Bytes of workspace (16-byte aligned) of the forward (op DCN_OP_FORWARD) or the
+ * backward (DCN_OP_BACKWARD); 0 for invalid params. */
+DCN_API size_t dcn_group_norm_workspace_size(const dcn_norm_params_t* params, int op);
+
+/* Writes y, and stats unless it is NULL. y may be x. */
+DCN_API int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const void* gamma,
+                                   const void* beta, void* y, float* stats, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Given grad_y [B, H, W, C] (dtype) and the forward's x and stats: grad_x in
+ * `dtype` (the gradient through mean and rstd included), grad_gamma and
+ * grad_beta [C] in float32. Each output may be NULL (not computed); grad_x may be
+ * grad_y. relu has slope 0 at 0. Equal calls give equal bits. */
+DCN_API int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, const void* gamma,
+                                    const void* beta, const float* stats, const void* grad_y, void* grad_x,
+                                    float* grad_gamma, float* grad_beta, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
 /* The calling thread's last error message ("" after success). */
 DCN_API const char* dcn_last_error_string(void);
 

@@ -1,0 +1,217 @@
+"""Group normalisation on the GPU against float64, forward and backward."""
+import pytest
+import torch
+
+import deformable_convolution_dcn_b200 as dcn
+import op_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+ACTS = ("none", "relu", "silu", "gelu")
+EPS = 1e-5
+# B, H, W, C, groups: one value a group, one pixel, odd channels, groups that straddle a vector, one group, a group
+# a channel, wide channels, groups wider than a block, long maps, many samples
+SIZES = [(1, 1, 1, 1, 1), (2, 1, 1, 64, 8), (3, 5, 7, 30, 3), (1, 7, 10, 256, 32), (2, 9, 13, 66, 6), (2, 8, 8, 24, 2),
+         (1, 6, 5, 40, 40), (2, 11, 3, 12, 1), (1, 50, 50, 256, 32), (2, 100, 90, 64, 16), (5, 4, 4, 2048, 32),
+         (1, 3, 3, 4104, 2), (1, 2, 5, 2049, 1), (1, 130, 257, 8, 1), (70, 3, 2, 16, 4), (2, 33, 31, 96, 32),
+         (1, 200, 210, 128, 32), (2, 40, 40, 520, 40), (1, 64, 64, 1088, 64)]
+
+
+def make(B, H, W, C, dtype, affine=True, level=0.7, seed=0):
+    g = torch.Generator().manual_seed(seed * 7919 + B * 31 + H * 17 + W * 5 + C)
+    t = TYPES[dtype]
+    n = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x = n(B, H, W, C) * (torch.rand(C, generator=g) + 0.5) + level * n(C)
+    d = dict(x=x.to(t).cuda(), gy=n(B, H, W, C).to(t).cuda(), ga=None, be=None)
+    if affine:
+        d.update(ga=(1 + 0.3 * n(C)).to(t).cuda(), be=(0.3 * n(C)).to(t).cuda())
+    return d
+
+
+def check_forward(d, groups, act, eps=EPS):
+    y, stats = dcn.group_norm_forward(d["x"], d["ga"], d["be"], groups, eps, act)
+    torch.cuda.synchronize()
+    dcn.check_status()
+    want = ref.norm_forward(d["x"], d["ga"], d["be"], groups, eps, act)
+    ref.check("mean", stats[..., 0], *want["mean"])
+    ref.check("rstd", stats[..., 1], *want["rstd"])
+    ref.check("y", y, *want["y"])
+    return y, stats
+
+
+def given_stats(d, groups, eps=EPS):
+    return torch.stack(ref.norm_stats(d["x"], groups, eps), dim=-1).float()
+
+
+def check_backward(d, groups, act):
+    stats = given_stats(d, groups)
+    got = dcn.group_norm_backward(d["x"], d["ga"], d["be"], stats, d["gy"], groups, act)
+    torch.cuda.synchronize()
+    dcn.check_status()
+    want = ref.norm_backward(d["x"], d["ga"], d["be"], stats, d["gy"], groups, act)
+    for name, v in zip(("grad_x", "grad_gamma", "grad_beta"), got):
+        if name == "grad_x" or d["ga"] is not None:
+            ref.check(name, v, *want[name])
+        else:
+            assert v is None
+    gx = dcn.group_norm_backward(d["x"], d["ga"], d["be"], stats, d["gy"], groups, act, need_params=False)
+    assert gx[1] is None and gx[2] is None and torch.equal(gx[0], got[0])
+    if d["ga"] is not None:
+        gp = dcn.group_norm_backward(d["x"], d["ga"], d["be"], stats, d["gy"], groups, act, need_input=False)
+        assert gp[0] is None and torch.equal(gp[1], got[1]) and torch.equal(gp[2], got[2])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
+def test_group_norm_forward_matches(size, dtype):
+    i = SIZES.index(size)
+    check_forward(make(*size[:4], dtype, affine=i % 4 != 2), size[4], ACTS[i % 4])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", SIZES, ids=["x".join(map(str, s)) for s in SIZES])
+def test_group_norm_backward_matches(size, dtype):
+    i = SIZES.index(size)
+    check_backward(make(*size[:4], dtype, affine=i % 4 != 3, seed=1), size[4], ACTS[(i + 1) % 4])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("act", ACTS)
+def test_group_norm_every_activation(act, dtype):
+    d = make(2, 12, 11, 48, dtype, seed=2)
+    check_forward(d, 6, act)
+    check_backward(d, 6, act)
+
+
+@pytest.mark.parametrize("size", [(2, 20, 20, 32), (1, 150, 140, 64)], ids=["small", "long"])
+def test_group_norm_level_far_from_zero(size):
+    """A level a thousand spreads from zero costs the digits that x itself has lost, no more."""
+    d = make(*size, "f32", seed=3)
+    d["x"] = d["x"] + 1000.0
+    check_forward(d, 4, "silu")
+    check_backward(d, 4, "none")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_group_norm_constant_groups(dtype):
+    """No spread at all: y = act(beta), rstd = 1 / sqrt(eps)."""
+    d = make(2, 6, 6, 32, dtype, seed=4)
+    d["x"] = torch.full_like(d["x"], 3.25)
+    y, stats = check_forward(d, 8, "none")
+    assert torch.equal(y, d["be"].expand_as(y))
+    assert torch.allclose(stats[..., 1], torch.full_like(stats[..., 1], EPS ** -0.5), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", [(2, 6, 7, 32), (2, 60, 70, 32)], ids=["small", "long"])
+def test_group_norm_infinity_and_nan_stay_in_their_group(size, dtype):
+    d = make(*size, dtype, seed=5)
+    clean, _ = dcn.group_norm_forward(d["x"], d["ga"], d["be"], 4, EPS, "silu")
+    d["x"][0, 2, 3, 9] = float("nan")
+    d["x"][1, 5, 0, 31] = float("inf")
+    d["x"][1, 0, 0, 0] = float("-inf")  # the first pixel, which sums are taken about
+    y, stats = dcn.group_norm_forward(d["x"], d["ga"], d["be"], 4, EPS, "silu")
+    torch.cuda.synchronize()
+    for b, g in ((0, 1), (1, 3), (1, 0)):
+        assert torch.isnan(y[b, ..., g * 8:g * 8 + 8]).all()
+        y[b, ..., g * 8:g * 8 + 8] = clean[b, ..., g * 8:g * 8 + 8]
+    assert torch.equal(y, clean)
+
+
+def test_group_norm_in_place_and_unaligned():
+    d = make(2, 9, 9, 48, "bf16", seed=6)
+    y, stats = check_forward(d, 6, "relu")
+    buf = d["x"].clone()
+    z, stats2 = dcn.group_norm_forward(buf, d["ga"], d["be"], 6, EPS, "relu", out=buf)
+    assert z.data_ptr() == buf.data_ptr() and torch.equal(z, y) and torch.equal(stats, stats2)
+    flat = torch.empty(d["x"].numel() + 1, dtype=torch.bfloat16, device="cuda")
+    for name in ("x", "gy"):
+        e = dict(d)
+        flat[1:] = d[name].flatten()
+        e[name] = flat[1:].view(d["x"].shape)
+        check_forward(e, 6, "silu")
+        check_backward(e, 6, "relu")
+    for dtype in TYPES:
+        e = make(1, 8, 9, 33, dtype, seed=7)
+        for k in ("ga", "be"):  # parameters that start on an element
+            e[k] = torch.cat([e[k][:1], e[k]])[1:]
+        check_forward(e, 11, "gelu")
+
+
+@pytest.mark.parametrize("size", [(2, 50, 50, 64), (3, 128, 128, 96)], ids=["small", "long"])
+def test_group_norm_calls_are_independent(size):
+    a, b = make(*size, "bf16", seed=8), make(*size, "bf16", seed=9)
+    run = lambda d: (*(f := dcn.group_norm_forward(d["x"], d["ga"], d["be"], 8, EPS, "silu")),  # noqa: E731
+                     *dcn.group_norm_backward(d["x"], d["ga"], d["be"], f[1], d["gy"], 8, "silu"))
+    wa, wb = run(a), run(b)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            ga = run(a)
+        with torch.cuda.stream(s2):
+            gb = run(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(ga + gb, wa + wb))
+    c = {k: v.clone() for k, v in a.items()}
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run(c)
+        graphs.append((g, out))
+    for d, want in ((a, wa), (b, wb)):
+        for k in c:
+            c[k].copy_(d[k])
+        torch.cuda.synchronize()
+        for (g, _), s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert all(torch.equal(u, v) for u, v in zip(out, want))
+    dcn.check_status()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_group_norm_gradients_against_differences(act):
+    d = make(2, 5, 6, 24, "f32", seed=10)
+    leaves = {k: d[k].requires_grad_() for k in ("x", "ga", "be")}
+    dcn.group_norm(leaves["x"], leaves["ga"], leaves["be"], 4, EPS, act).backward(d["gy"])
+
+    def loss(v):
+        mean, rstd = ref.norm_stats(v["x"], 4, EPS)
+        z = (v["x"] - ref._spread(mean, 24)) * ref._spread(rstd, 24) * v["ga"] + v["be"]
+        return float((ref.act(z, act) * d["gy"].double()).sum())
+
+    g = torch.Generator(device="cuda").manual_seed(11)
+    base = {k: v.detach().double() for k, v in leaves.items()}
+    h = 1e-6
+    for k in leaves:
+        v = torch.randn(base[k].shape, generator=g, device="cuda", dtype=torch.float64)
+        slope = (loss({**base, k: base[k] + h * v}) - loss({**base, k: base[k] - h * v})) / (2 * h)
+        got = float((leaves[k].grad.double() * v).sum())
+        size = float((leaves[k].grad.double() * v).abs().sum())
+        assert abs(got - slope) <= 1e-4 * size + 1e-6, k
+
+
+def test_group_norm_refusals_on_the_device():
+    d = make(2, 4, 4, 16, "bf16")
+    with pytest.raises(dcn.DcnError, match="multiple of groups"):
+        dcn.group_norm_forward(d["x"], None, None, 3)
+    with pytest.raises(dcn.DcnError, match="groups"):
+        dcn.group_norm_forward(d["x"], None, None, 0)
+    with pytest.raises(dcn.DcnError, match="eps"):
+        dcn.group_norm_forward(d["x"], None, None, 4, eps=0.0)
+    with pytest.raises(ValueError, match="gamma"):
+        dcn.group_norm_forward(d["x"], d["ga"][:-1], None, 4)
+    with pytest.raises(ValueError, match="contiguous"):
+        dcn.group_norm_forward(d["x"].permute(0, 2, 1, 3), None, None, 4)
+    with pytest.raises(ValueError, match="stats"):
+        dcn.group_norm_backward(d["x"], None, None, torch.zeros(2, 3, 2, device="cuda"), d["gy"], 4)
+    ws = torch.empty(8, dtype=torch.uint8, device="cuda")
+    p = dcn._norm_params(d["x"], 4, EPS, "none")
+    if dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD) > 8:
+        with pytest.raises(dcn.DcnError, match="workspace"):
+            dcn.group_norm_backward(d["x"], None, None, given_stats(d, 4), d["gy"], 4, workspace=ws)

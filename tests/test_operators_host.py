@@ -1,0 +1,144 @@
+"""Host-side checks of the linear layer and the group normalisation (no GPU
+needed): bad arguments are rejected with the documented codes before anything
+reaches the device. No call here passes valid device pointers."""
+import ctypes
+
+import pytest
+import torch
+
+import deformable_convolution_dcn_b200 as dcn
+
+OK, EINVAL, EUNSUP, EWS = 0, -1, -2, -5
+F = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 1)
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from deformable_convolution_dcn_b200 import build
+    build.build()
+    return dcn._load()
+
+
+def LP(**kw):
+    d = dict(M=5, N=6, K=7, act=1, dtype=1, flags=0)
+    d.update(kw)
+    return dcn.LinearParams(*(d[k] for k in ("M", "N", "K", "act", "dtype", "flags")))
+
+
+def NP(**kw):
+    d = dict(B=2, H=3, W=4, C=12, groups=3, eps=1e-5, act=1, dtype=1, flags=0)
+    d.update(kw)
+    return dcn.NormParams(*(d[k] for k in ("B", "H", "W", "C", "groups", "eps", "act", "dtype", "flags")))
+
+
+def lin_fwd(lib, p, x=F, w=F, b=None, r=None, y=F, z=None, ws=F, n=BIG):
+    return lib.dcn_linear_forward(ctypes.byref(p), x, w, b, r, y, z, ws, n, None)
+
+
+def lin_bwd(lib, p, x=F, w=F, s=F, gy=F, gx=F, gw=F, gb=F, gr=F, ws=F, n=BIG):
+    return lib.dcn_linear_backward(ctypes.byref(p), x, w, s, gy, gx, gw, gb, gr, ws, n, None)
+
+
+def gn_fwd(lib, p, x=F, ga=None, be=None, y=F, st=F, ws=F, n=BIG):
+    return lib.dcn_group_norm_forward(ctypes.byref(p), x, ga, be, y, st, ws, n, None)
+
+
+def gn_bwd(lib, p, x=F, ga=None, be=None, st=F, gy=F, gx=F, gg=F, gb=F, ws=F, n=BIG):
+    return lib.dcn_group_norm_backward(ctypes.byref(p), x, ga, be, st, gy, gx, gg, gb, ws, n, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(act=4), EINVAL), (dict(act=-1), EINVAL),
+    (dict(dtype=2), EUNSUP), (dict(M=1 << 20, N=1 << 12), EUNSUP), (dict(M=1 << 20, K=1 << 12), EUNSUP),
+    (dict(N=1 << 20, K=1 << 12), EUNSUP),
+])
+def test_linear_params_rejected(lib, bad, code):
+    p = LP(**bad)
+    assert lin_fwd(lib, p) == code
+    assert lib.dcn_last_error_string().decode() != ""
+    assert lin_bwd(lib, p) == code
+    assert dcn.linear_workspace_size(p, dcn.OP_FORWARD) == 0
+    assert dcn.linear_workspace_size(p, dcn.OP_BACKWARD) == 0
+
+
+def test_linear_pointers(lib):
+    p = LP()
+    for kw in (dict(x=None), dict(w=None), dict(y=None)):
+        assert lin_fwd(lib, p, **kw) == EINVAL
+    for kw in (dict(x=ODD), dict(w=ODD), dict(b=ODD), dict(r=ODD), dict(y=ODD), dict(z=ODD)):
+        assert lin_fwd(lib, p, **kw) == EUNSUP
+    for kw in (dict(x=None), dict(w=None), dict(s=None), dict(gy=None)):
+        assert lin_bwd(lib, p, **kw) == EINVAL
+    for kw in (dict(s=ODD), dict(gy=ODD), dict(gx=ODD), dict(gw=ctypes.c_void_p((1 << 20) + 2)), dict(gr=ODD)):
+        assert lin_bwd(lib, p, **kw) == EUNSUP
+    assert lib.dcn_linear_forward(None, F, F, None, None, F, None, None, 0, None) == EINVAL
+
+
+def test_linear_without_rows_or_outputs_enqueues_nothing(lib):
+    n = dcn.launch_count()
+    assert lin_fwd(lib, LP(M=0), x=None, y=None) == OK
+    assert lin_bwd(lib, LP(), gx=None, gw=None, gb=None, gr=None) == OK
+    assert lin_bwd(lib, LP(M=0), x=None, s=None, gy=None, gw=None, gb=None) == OK
+    assert dcn.launch_count() == n
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(B=0), EINVAL), (dict(H=0), EINVAL), (dict(W=-2), EINVAL), (dict(C=0), EINVAL), (dict(groups=0), EINVAL),
+    (dict(groups=5), EINVAL), (dict(eps=0.0), EINVAL), (dict(eps=float("nan")), EINVAL),
+    (dict(eps=float("inf")), EINVAL), (dict(act=9), EINVAL), (dict(dtype=3), EUNSUP),
+    (dict(B=1 << 10, H=1 << 10, W=1 << 10), EUNSUP),
+])
+def test_group_norm_params_rejected(lib, bad, code):
+    p = NP(**bad)
+    assert gn_fwd(lib, p) == code
+    assert lib.dcn_last_error_string().decode() != ""
+    assert gn_bwd(lib, p) == code
+    assert dcn.group_norm_workspace_size(p, dcn.OP_FORWARD) == 0
+    assert dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD) == 0
+
+
+def test_group_norm_pointers_and_workspace(lib):
+    p = NP()
+    for kw in (dict(x=None), dict(y=None)):
+        assert gn_fwd(lib, p, **kw) == EINVAL
+    for kw in (dict(x=ODD), dict(ga=ODD), dict(be=ODD), dict(y=ODD), dict(st=ctypes.c_void_p((1 << 20) + 2))):
+        assert gn_fwd(lib, p, **kw) == EUNSUP
+    for kw in (dict(x=None), dict(st=None), dict(gy=None)):
+        assert gn_bwd(lib, p, **kw) == EINVAL
+    assert gn_bwd(lib, p, gx=None, gg=None, gb=None) == OK
+    for op, call in ((dcn.OP_FORWARD, gn_fwd), (dcn.OP_BACKWARD, gn_bwd)):
+        n = dcn.group_norm_workspace_size(p, op)
+        if n:
+            assert call(lib, p, ws=None) == EWS
+            assert call(lib, p, n=n - 1) == EWS
+            assert str(n) in lib.dcn_last_error_string().decode()
+            assert call(lib, p, ws=ctypes.c_void_p((1 << 20) + 8)) == EUNSUP
+
+
+def test_binding_rejects_shapes():
+    x, w = torch.zeros(2, 3, 8), torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        dcn.linear_forward(x, w)
+    with pytest.raises(ValueError, match="weight"):
+        dcn.linear_forward(x, torch.zeros(4, 9))
+    with pytest.raises(ValueError, match="1, 1"):
+        dcn.linear_forward(x, torch.zeros(4, 3, 3, 8))
+    with pytest.raises(ValueError, match="empty"):
+        dcn.linear_forward(torch.zeros(2, 0), torch.zeros(4, 0))
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        dcn.linear_forward(x.half(), w.half())
+    with pytest.raises(ValueError, match="activation"):
+        dcn.linear_forward(x, w, activation="tanh")
+    with pytest.raises(ValueError, match="saved must be None"):
+        dcn.linear_backward(x, w, x, x, "none")
+    with pytest.raises(ValueError, match="saved must be the output"):
+        dcn.linear_backward(x, w, None, x, "relu")
+    m = torch.zeros(1, 2, 2, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        dcn.group_norm_forward(m, None, None, 2)
+    with pytest.raises(ValueError, match="B, H, W, C"):
+        dcn.group_norm_forward(x, None, None, 2)
+    with pytest.raises(ValueError, match="activation"):
+        dcn.group_norm_forward(m, None, None, 2, activation="elu")
