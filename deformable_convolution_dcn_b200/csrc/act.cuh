@@ -8,6 +8,14 @@
 
 namespace dcn {
 
+// One element as float32. Loads through a pointer that may be null use this and
+// not ldf(): the header's __ldg of a bfloat16 is an inline assembly statement
+// that the compiler may move ahead of the test of the pointer, which faults.
+__device__ __forceinline__ float ld1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float ld1(const bf16* p) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
+}
+
 // dcn_act_t values
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
 

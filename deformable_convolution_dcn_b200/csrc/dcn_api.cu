@@ -581,8 +581,25 @@ size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op) {
         g_err = keep;
         return 0;
     }
-    (void)op;
-    return 0;
+    if ((params->flags & DCN_FLAG_GENERIC) || s.M == 0) return 0;
+    return dcn::linear_tc_workspace(s, params->dtype == DCN_BF16, op == DCN_OP_BACKWARD);
+}
+
+// The tensor-core kernels read matrices of 16-byte aligned rows in place and copy the others; only an unaligned base
+// of one read in place sends a layer to the CUDA-core kernels, which need no workspace.
+static bool use_linear_tc(const dcn_linear_params_t* p, const dcn::LinearShape& s, const void* x, const void* w,
+                          const void* gy) {
+    bool in_xw, in_gy;
+    dcn::linear_tc_in_place(s, p->dtype == DCN_BF16, &in_xw, &in_gy);
+    return !(p->flags & DCN_FLAG_GENERIC) && (!in_xw || (aligned16(x) && aligned16(w))) && (!in_gy || aligned16(gy));
+}
+
+static int linear_workspace_ok(const dcn_linear_params_t* params, int op, const void* workspace, size_t bytes) {
+    const size_t need = dcn_linear_workspace_size(params, op);
+    if (need > 0 && (!workspace || bytes < need))
+        return fail(DCN_ERR_WORKSPACE, "the linear layer needs %zu bytes of workspace, got %zu", need,
+                    workspace ? bytes : (size_t)0);
+    return check_ptr(workspace, "workspace", 256, need > 0);
 }
 
 int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const void* weight, const void* bias,
@@ -599,8 +616,18 @@ int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const v
     TRY(check_ptr(y, "y", es, any));
     TRY(check_ptr(z, "z", es, false));
     if (!any) return ok();
-    (void)workspace, (void)workspace_bytes;
     int n = 0;
+    if (use_linear_tc(params, s, x, weight, nullptr)) {
+        TRY(linear_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+        unsigned* status = nullptr;
+        cudaError_t e = dcn::status_word_ptr(&status);
+        if (e != cudaSuccess) return cuda_fail(e, "status word");
+        e = dcn::linear_tc_forward(s, params->dtype == DCN_BF16, x, weight, bias, residual, y, z, workspace, status,
+                                   (cudaStream_t)stream, &n);
+        g_launches += n;
+        if (e != cudaSuccess) return cuda_fail(e, "tensor-core linear forward launch");
+        return ok();
+    }
     cudaError_t e = dcn::linear_forward(s, params->dtype == DCN_BF16, x, weight, bias, residual, y, z,
                                         (cudaStream_t)stream, &n);
     g_launches += n;
@@ -624,9 +651,20 @@ int dcn_linear_backward(const dcn_linear_params_t* params, const void* x, const 
     TRY(check_ptr(grad_weight, "grad_weight", 4, false));
     TRY(check_ptr(grad_bias, "grad_bias", 4, false));
     TRY(check_ptr(grad_residual, "grad_residual", es, false));
-    (void)workspace, (void)workspace_bytes;
-    if (!any) grad_x = grad_residual = nullptr;  // no rows; grad_weight and grad_bias are zero
+    if (!grad_x && !grad_weight && !grad_bias && !grad_residual) return ok();
+    if (!any) grad_x = nullptr, grad_residual = nullptr;  // no rows; grad_weight and grad_bias are zero
     int n = 0;
+    if (any && use_linear_tc(params, s, x, weight, grad_y)) {
+        TRY(linear_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+        unsigned* status = nullptr;
+        cudaError_t e = dcn::status_word_ptr(&status);
+        if (e != cudaSuccess) return cuda_fail(e, "status word");
+        e = dcn::linear_tc_backward(s, params->dtype == DCN_BF16, x, weight, saved, grad_y, grad_x, grad_weight,
+                                    grad_bias, grad_residual, workspace, status, (cudaStream_t)stream, &n);
+        g_launches += n;
+        if (e != cudaSuccess) return cuda_fail(e, "tensor-core linear backward launch");
+        return ok();
+    }
     cudaError_t e = dcn::linear_backward(s, params->dtype == DCN_BF16, x, weight, saved, grad_y, grad_x, grad_weight,
                                          grad_bias, grad_residual, (cudaStream_t)stream, &n);
     g_launches += n;

@@ -103,7 +103,7 @@ __device__ __forceinline__ Cols cols_of(const NormShape& s, const Plan& p, int b
 template <typename T, int V>
 __device__ __forceinline__ void load(float (&v)[V], const T* p) {
     if constexpr (V == 1) {
-        v[0] = ldf(p);
+        v[0] = ld1(p);
     } else if constexpr (V == 4) {
         const float4 q = __ldg(reinterpret_cast<const float4*>(p));
         v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(NT) stats_kernel(const NormShape s, const Plan
             d += sm[(ty + r) * p.cb + q];
         }
         const float m = a / n;  // about the first pixel
-        sm[q] = ldf(x + ((size_t)b * s.HW + r0) * s.C + c.c0 + q) + m;  // row 0's sums were this thread's alone
+        sm[q] = ld1(x + ((size_t)b * s.HW + r0) * s.C + c.c0 + q) + m;  // row 0's sums were this thread's alone
         const float m2 = d - a * m;
         sm[ty * p.cb + q] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
     }
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(NT) apply_kernel(const NormShape s, const Plan
     for (int i = 0; i < V; ++i) {
         const int ch = cx * V + i, g = p.gpb ? ch / cg : 0;
         mean[i] = sm[g];
-        a[i] = sm[ngp + g] * (gamma ? ldf(gamma + c.c0 + ch) : 1.f);
-        be[i] = beta ? ldf(beta + c.c0 + ch) : 0.f;
+        a[i] = sm[ngp + g] * (gamma ? ld1(gamma + c.c0 + ch) : 1.f);
+        be[i] = beta ? ld1(beta + c.c0 + ch) : 0.f;
     }
     const int r1 = min((chunk + 1) * p.rows, s.HW);
     const size_t at = (size_t)b * s.HW * s.C + c.c0 + cx * V;
@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(NT) bwd_sums_kernel(const NormShape s, const P
             const float* st = stats + ((size_t)b * s.groups + ch / cg) * 2;
             mean[i] = __ldg(st);
             rstd[i] = __ldg(st + 1);
-            ga[i] = gamma ? ldf(gamma + ch) : 1.f;
-            be[i] = beta ? ldf(beta + ch) : 0.f;
+            ga[i] = gamma ? ld1(gamma + ch) : 1.f;
+            be[i] = beta ? ld1(beta + ch) : 0.f;
         }
         const size_t at = (size_t)b * s.HW * s.C + c.c0 + cx * V;
 #pragma unroll 2
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(NT) bwd_apply_kernel(const NormShape s, const 
         for (int i = lane; i < p.chunks * cg; i += 32) {
             const int ch = (c.g0 + g) * cg + i % cg;
             const float2 q = sums[((size_t)b * p.chunks + i / cg) * s.C + ch];
-            const float ga = gamma ? ldf(gamma + ch) : 1.f;
+            const float ga = gamma ? ld1(gamma + ch) : 1.f;
             a = fmaf(ga, q.x, a);
             d = fmaf(ga, q.y, d);
         }
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(NT) bwd_apply_kernel(const NormShape s, const 
         const float* st = stats + ((size_t)b * s.groups + ch / cg) * 2;
         mean[i] = __ldg(st);
         rstd[i] = __ldg(st + 1);
-        ga[i] = gamma ? ldf(gamma + ch) : 1.f;
-        be[i] = beta ? ldf(beta + ch) : 0.f;
+        ga[i] = gamma ? ld1(gamma + ch) : 1.f;
+        be[i] = beta ? ld1(beta + ch) : 0.f;
         c1[i] = sm[g];
         c2[i] = sm[ngp + g];
     }

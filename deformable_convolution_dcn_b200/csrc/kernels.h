@@ -124,6 +124,18 @@ cudaError_t linear_forward(const LinearShape& s, int dtype_bf16, const void* x, 
 cudaError_t linear_backward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* saved,
                             const void* gy, void* gx, float* gw, float* gb, void* gr, cudaStream_t st, int* launches);
 
+// linear_tc.cu — the same layer on tcgen05 tensor cores. Matrices that the tensor maps read in place (see
+// linear_tc_in_place) are 16-byte aligned, ws 256-byte aligned.
+size_t linear_tc_workspace(const LinearShape& s, int dtype_bf16, bool backward);
+cudaError_t linear_tc_forward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* bias,
+                              const void* residual, void* y, void* z, void* ws, unsigned* status, cudaStream_t st,
+                              int* launches);
+cudaError_t linear_tc_backward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* saved,
+                               const void* gy, void* gx, float* gw, float* gb, void* gr, void* ws, unsigned* status,
+                               cudaStream_t st, int* launches);
+// x and w (in_gy: grad_y) are read in place, not through a copy in the workspace.
+void linear_tc_in_place(const LinearShape& s, int dtype_bf16, bool* in_xw, bool* in_gy);
+
 // group_norm.cu — group normalisation with an activation, channels last. vec: x, y, grad_y and
 // grad_x are 16-byte aligned.
 struct NormShape {

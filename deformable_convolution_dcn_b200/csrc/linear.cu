@@ -20,7 +20,7 @@ template <typename T>
 struct Plain {  // element (i, r) of a matrix, or of its transpose
     const T* p;
     long long si, sr;
-    __device__ float operator()(long long i, long long r) const { return ldf(p + i * si + r * sr); }
+    __device__ float operator()(long long i, long long r) const { return ld1(p + i * si + r * sr); }
 };
 
 template <typename T, int ACT>
@@ -29,9 +29,9 @@ struct Dz {  // dz(i, r), or transposed
     long long si, sr;
     __device__ float operator()(long long i, long long r) const {
         const long long at = i * si + r * sr;
-        const float g = ldf(gy + at);
+        const float g = ld1(gy + at);
         if constexpr (ACT == kActNone) return g;
-        return act_grad<ACT>(g, ldf(saved + at));
+        return act_grad<ACT>(g, ld1(saved + at));
     }
 };
 
@@ -42,8 +42,8 @@ struct Epilogue {  // bias, residual, pre-activation, activation
     long long ld;
     __device__ void operator()(long long i, long long j, float v) const {
         const long long at = i * ld + j;
-        if (bias) v += ldf(bias + j);
-        if (residual) v += ldf(residual + at);
+        if (bias) v += ld1(bias + j);
+        if (residual) v += ld1(residual + at);
         if (z) z[at] = from_float<T>(v);
         y[at] = from_float<T>(act_apply<ACT>(v));
     }

@@ -1,0 +1,979 @@
+// The linear layer's matrix products on sm_100a tensor cores:
+//   forward      D[m, n] = sum_k x[m, k] W[n, k]      both operands K-major
+//   grad_x       D[m, k] = sum_n dz[m, n] W[n, k]     W MN-major
+//   grad_weight  D[n, k] = sum_m dz[m, n] x[m, k]     both MN-major
+// One persistent kernel computes them all, D = A B^T with A's rows on the TMEM
+// lanes (128 a CTA) and BN of B's rows on its columns. Either matrix may take
+// A's place; D is then written transposed (products of few rows put the long
+// side on the lanes). CG = 2 runs two CTAs as one tile of 256 rows (cta_group::2),
+// each holding half of B's rows, which halves the L2 traffic of B.
+//
+// float32 accuracy from bfloat16 products: a float32 operand is split beforehand
+// in three bfloat16 terms a0 + a1 + a2 (24 bits), and the product is
+// a0 b0 + (a0 b1 + a1 b0 + a1 b1 + a0 b2 + a2 b0); the terms left out are below
+// 2^-26 of a b. a0 b0 has an accumulator of its own, so that the small products
+// do not make it round more often. The tensor cores cut each step's sum off
+// rather than rounding it, so float32 results take the accumulator out every
+// `chunk` blocks of 64 and add it in registers with proper rounding.
+//
+// Warps: 0 TMA producer, 1 MMA issue and TMEM, 2-9 epilogue (each of the four
+// TMEM lane quarters twice, once for each half of the columns). Accumulators
+// are double buffered: the epilogue of a tile overlaps the next one's MMAs. The
+// epilogue adds bias and residual, applies the activation and stores whole
+// 32-byte sectors. Products with too few tiles to fill the GPU are split along
+// the reduction; the parts meet in reduce_kernel, in a fixed order.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "act.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace dcn {
+namespace {
+
+constexpr int BM = 128, BK = 64;          // lanes a CTA, reduction elements a stage
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + EPI_WARPS * 32;
+constexpr int MAX_STAGES = 8;
+constexpr uint32_t A_BYTES = BM * BK * 2; // one term of one stage
+constexpr uint32_t MN_BLOCK = BK * 128;   // 64 rows of an MN-major operand over a stage: 8 KB
+constexpr uint32_t SMEM_MAX = 227 * 1024, BAR_BYTES = 256;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr long long WAIT_LIMIT = 2000000000LL;
+
+struct GemmArgs {
+    int rows, cols;        // D: A-side rows, B-side rows
+    int kblocks, splits;   // stages of 64; parts along the reduction
+    int chunk;             // stages between two reads of the accumulator
+    int mt, nt;            // tiles
+    int bn;                // B rows a tile (of the CTA or pair)
+    int ta, tb;            // bfloat16 terms of A, B
+    int a_mn, b_mn;        // operand is MN-major
+    int stages;
+    uint32_t stage_bytes, bar_off;
+    // epilogue: D[i, j] goes to element i * rs + j * cs
+    long long rs, cs, part;  // part: elements between two splits' results
+    const void *bias, *residual;
+    void *y, *z;
+    int act;
+    int vec;               // 2 / 1: rows of D are 32- / 16-byte aligned; 0: element by element
+    unsigned* status;
+};
+
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int mn, int k) {
+    // K-major: 16 reduction elements on = 32 bytes on; MN-major: 16 rows of 128 bytes on,
+    // blocks of 64 rows MN_BLOCK apart (leading byte offset)
+    uint64_t d = ptx::sw128_desc(addr + (mn ? k * 2048 : k * 32));
+    if (mn) d = (d & ~((uint64_t)0x3FFFu << 16)) | ((uint64_t)(MN_BLOCK >> 4) << 16);
+    return d;
+}
+
+__device__ __forceinline__ float act_run(float z, int act) {
+    switch (act) {
+        case kActRelu: return act_apply<kActRelu>(z);
+        case kActSilu: return act_apply<kActSilu>(z);
+        case kActGelu: return act_apply<kActGelu>(z);
+        default: return z;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_apply<ACT>(v[i]);
+}
+
+template <typename T>
+struct Pack32;  // 32 values of a row <-> 32-byte vectors
+template <>
+struct Pack32<float> {
+    static constexpr int N = 32;  // words
+    static __device__ __forceinline__ void put(uint32_t (&w)[32], const float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+    }
+    static __device__ __forceinline__ void add(float (&v)[32], const uint32_t (&w)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(w[i]);
+    }
+};
+template <>
+struct Pack32<bf16> {
+    static constexpr int N = 16;
+    static __device__ __forceinline__ void put(uint32_t (&w)[16], const float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    static __device__ __forceinline__ void add(float (&v)[32], const uint32_t (&w)[16]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[2 * i] += __uint_as_float(w[i] << 16);
+            v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void load_row(uint32_t (&w)[N], const void* p, int vec) {
+    if (vec == 2) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            ptx::ldg_v8(*reinterpret_cast<uint32_t(*)[8]>(&w[i]), static_cast<const char*>(p) + i * 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "l"(static_cast<const char*>(p) + i * 4));
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_row(void* p, const uint32_t (&w)[N], int vec) {
+    if (vec == 2) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            ptx::stg_v8(static_cast<char*>(p) + i * 4, *reinterpret_cast<const uint32_t(*)[8]>(&w[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+
+// The epilogue of 32 columns of one row of D.
+template <typename T>
+struct Emit {
+    const GemmArgs& a;
+    T *y, *z;
+    const T *bias, *residual;
+    int row;
+    __device__ __forceinline__ bool whole(int col) const { return a.vec && row < a.rows && col + 32 <= a.cols; }
+    // residual values ahead of the accumulator
+    __device__ __forceinline__ void ahead(uint32_t (&r)[Pack32<T>::N], int col) const {
+        if (residual && whole(col)) load_row(r, residual + row * a.rs + col, a.vec);
+    }
+    __device__ __forceinline__ void plain(const float (&v)[32], int col) const {
+        if (whole(col)) {
+            uint32_t w[Pack32<T>::N];
+            Pack32<T>::put(w, v);
+            store_row(y + row * a.rs + col, w, a.vec);
+        } else if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i < a.cols) y[row * a.rs + (col + i) * a.cs] = from_float<T>(v[i]);
+        }
+    }
+    __device__ __forceinline__ void operator()(float (&v)[32], const uint32_t (&r)[Pack32<T>::N], int col) const {
+        if (bias) {
+            if (a.cs == 1) {  // bias by column: one coalesced load, spread by shuffles (all lanes are here)
+                const int c = col + (int)(threadIdx.x & 31);
+                const float b = c < a.cols ? ld1(bias + c) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(~0u, b, i);
+            } else {
+                const float b = row < a.rows ? ld1(bias + row) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += b;
+            }
+        }
+        if (whole(col)) {
+            const long long at = row * a.rs + col;
+            if (residual) Pack32<T>::add(v, r);
+            uint32_t w[Pack32<T>::N];
+            if (z) {
+                Pack32<T>::put(w, v);
+                store_row(z + at, w, a.vec);
+            }
+            switch (a.act) {
+                case kActRelu: act32<kActRelu>(v); break;
+                case kActSilu: act32<kActSilu>(v); break;
+                case kActGelu: act32<kActGelu>(v); break;
+                default: break;
+            }
+            Pack32<T>::put(w, v);
+            store_row(y + at, w, a.vec);
+        } else if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i < a.cols) {
+                    const long long at = row * a.rs + (col + i) * a.cs;
+                    float s = v[i];
+                    if (residual) s += ld1(residual + at);
+                    if (z) z[at] = from_float<T>(s);
+                    y[at] = from_float<T>(act_run(s, a.act));
+                }
+        }
+    }
+};
+
+// T: element type of D. PB: 0, or BN where the accumulator is added up in registers.
+template <typename T, int PB, int CG>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb, const GemmArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CG == 2 ? (int)ptx::cluster_ctarank() : 0;
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.bar_off);
+    const uint32_t full = ptx::smem_u32(bars), empty = full + MAX_STAGES * 8;
+    const uint32_t accfull = empty + MAX_STAGES * 8, accempty = accfull + 16, done = accempty + 16;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 5);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    const uint32_t base = ptx::smem_u32(smem);
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (tid == 0) {
+        for (int i = 0; i < MAX_STAGES; ++i) {
+            ptx::mbar_init(full + i * 8, 1);
+            ptx::mbar_init(empty + i * 8, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(accfull + i * 8, 1);
+            ptx::mbar_init(accempty + i * 8, EPI_WARPS * CG);
+        }
+        ptx::mbar_init(done, 1);
+        *s_abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tma);
+        ptx::prefetch_tmap(&tmb);
+    }
+    if (warp == 1) ptx::tmem_alloc_cg<CG>(ptx::smem_u32(s_tmem), TMEM_COLS);
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) ptx::cluster_sync();  // the pair's barriers are ready
+    ptx::tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    // a programmatic dependent of the stream's previous work: nothing global is touched before it is complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int units = a.mt * a.nt * a.splits;
+    auto unit_of = [&](int u, int& im, int& in, int& k0, int& k1, int& sp) {
+        sp = u % a.splits;
+        const int t = u / a.splits;
+        in = t % a.nt;
+        im = t / a.nt;
+        k0 = (int)((long long)a.kblocks * sp / a.splits);
+        k1 = (int)((long long)a.kblocks * (sp + 1) / a.splits);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- TMA producer: this CTA's rows of A, its share of B's rows
+            const int bn = a.bn / CG;
+            int it = 0;
+            bool ok = true;
+            for (int u = group; u < units && ok; u += groups) {
+                int im, in, k0, k1, sp;
+                unit_of(u, im, in, k0, k1, sp);
+                const int r0 = (im * CG + rank) * BM, c0 = in * a.bn + rank * bn;
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = it % a.stages;
+                    if (it >= a.stages)
+                        ok = ptx::mbar_wait(empty + s * 8, ((it / a.stages) - 1) & 1, s_abort, a.status, WAIT_LIMIT);
+                    if (!ok) break;
+                    const uint32_t bar = full + s * 8;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, a.stage_bytes * CG);
+                    uint32_t dst = base + s * a.stage_bytes;
+                    for (int t = 0; t < a.ta; ++t, dst += A_BYTES) {
+                        if (a.a_mn) {
+                            ptx::tma_load_3d<CG>(dst, &tma, bar, r0, kb * BK, t);
+                            ptx::tma_load_3d<CG>(dst + MN_BLOCK, &tma, bar, r0 + 64, kb * BK, t);
+                        } else {
+                            ptx::tma_load_3d<CG>(dst, &tma, bar, kb * BK, r0, t);
+                        }
+                    }
+                    for (int t = 0; t < a.tb; ++t, dst += bn * 128) {
+                        if (a.b_mn) {
+                            for (int h = 0; h < bn / 64; ++h)
+                                ptx::tma_load_3d<CG>(dst + h * MN_BLOCK, &tmb, bar, c0 + h * 64, kb * BK, t);
+                        } else {
+                            ptx::tma_load_3d<CG>(dst, &tmb, bar, kb * BK, c0, t);
+                        }
+                    }
+                }
+            }
+            // copies still in flight land before the CTA may exit (bounded)
+            if (rank == 0) {
+                volatile int none = 0;
+                for (int k = std::max(0, it - a.stages); k < it; ++k)
+                    ptx::mbar_wait(full + (k % a.stages) * 8, (k / a.stages) & 1, &none, nullptr, WAIT_LIMIT);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---- MMA issue
+            const uint32_t idesc =
+                ptx::idesc_bf16_f32(BM * CG, a.bn) | ((uint32_t)a.a_mn << 15) | ((uint32_t)a.b_mn << 16);
+            const uint32_t bterm = (uint32_t)(a.bn / CG) * 128;
+            int it = 0, ci = 0;
+            bool ok = true;
+            for (int u = group; u < units && ok; u += groups) {
+                int im, in, k0, k1, sp;
+                unit_of(u, im, in, k0, k1, sp);
+                for (int c0 = k0; c0 < k1 && ok; c0 += a.chunk, ++ci) {
+                    const int buf = ci & 1;
+                    if (ci >= 2) {
+                        ok = ptx::mbar_wait(accempty + buf * 8, ((ci >> 1) - 1) & 1, s_abort, a.status, WAIT_LIMIT);
+                        if (!ok) break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t acc = tmem + buf * 256, low = acc + 128;
+                    const int c1 = min(c0 + a.chunk, k1);
+                    for (int kb = c0; kb < c1; ++kb, ++it) {
+                        const int s = it % a.stages;
+                        ok = ptx::mbar_wait(full + s * 8, (it / a.stages) & 1, s_abort, a.status, WAIT_LIMIT);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t as = base + s * a.stage_bytes, bs = as + a.ta * A_BYTES;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t a0 = operand_desc(as, a.a_mn, k), b0 = operand_desc(bs, a.b_mn, k);
+                            const uint32_t more = (kb > c0 || k > 0) ? 1u : 0u;
+                            ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
+                            if (a.ta > 1) {
+                                const uint64_t a1 = operand_desc(as + A_BYTES, a.a_mn, k);
+                                const uint64_t a2 = operand_desc(as + 2 * A_BYTES, a.a_mn, k);
+                                ptx::mma_bf16_cg<CG>(low, a2, b0, idesc, more);
+                                ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, 1u);
+                                if (a.tb > 1) {
+                                    const uint64_t b1 = operand_desc(bs + bterm, a.b_mn, k);
+                                    const uint64_t b2 = operand_desc(bs + 2 * bterm, a.b_mn, k);
+                                    ptx::mma_bf16_cg<CG>(low, a0, b2, idesc, 1u);
+                                    ptx::mma_bf16_cg<CG>(low, a1, b1, idesc, 1u);
+                                    ptx::mma_bf16_cg<CG>(low, a0, b1, idesc, 1u);
+                                }
+                            }
+                        }
+                        ptx::mma_commit_cg<CG>(empty + s * 8);
+                    }
+                    ptx::mma_commit_cg<CG>(accfull + buf * 8);
+                }
+            }
+            // every issued MMA has completed before TMEM and shared memory are released (bounded)
+            volatile int none = 0;
+            ptx::mma_commit_cg<CG>(done);
+            ptx::mbar_wait(done, 0, &none, a.status, WAIT_LIMIT);
+        }
+    } else {
+        // ---- epilogue: quarter q of the lanes, half h of the columns
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const int half = a.bn / 2;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * half;
+        int ci = 0;
+        bool ok = true;
+        for (int u = group; u < units && ok; u += groups) {
+            int im, in, k0, k1, sp;
+            unit_of(u, im, in, k0, k1, sp);
+            const int col0 = in * a.bn + h * half;
+            const Emit<T> emit{a, (T*)a.y + sp * a.part, (T*)a.z, (const T*)a.bias, (const T*)a.residual,
+                               (im * CG + rank) * BM + q * 32 + lane};
+            uint32_t res[Pack32<T>::N];
+            if constexpr (PB == 0) {
+                emit.ahead(res, col0);
+                const int buf = ci & 1;
+                ok = ptx::mbar_wait(accfull + buf * 8, (ci >> 1) & 1, s_abort, a.status, WAIT_LIMIT);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                for (int j = 0; j < half; j += 32) {
+                    float v[32];
+                    ptx::tmem_ld32(lanes + buf * 256 + j, v);
+                    if (j + 32 >= half) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cg<CG>(accempty + buf * 8);
+                    }
+                    emit(v, res, col0 + j);
+                    if (j + 32 < half) emit.ahead(res, col0 + j + 32);
+                }
+                ++ci;
+            } else {
+                float acc[PB / 2] = {};
+                for (int c0 = k0; c0 < k1; c0 += a.chunk, ++ci) {
+                    const int buf = ci & 1;
+                    ok = ptx::mbar_wait(accfull + buf * 8, (ci >> 1) & 1, s_abort, a.status, WAIT_LIMIT);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < PB / 2; j += 32) {
+                        float v[32];
+                        ptx::tmem_ld32(lanes + buf * 256 + j, v);
+                        if (PB <= 128 && a.ta > 1) {
+                            float w[32];
+                            ptx::tmem_ld32(lanes + buf * 256 + 128 + j, w);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += w[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[j + i] += v[i];
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cg<CG>(accempty + buf * 8);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < PB / 2; j += 32) {
+                    float(&v)[32] = *reinterpret_cast<float(*)[32]>(&acc[j]);
+                    if constexpr (PB == 256) {  // grad_weight, one term: no epilogue
+                        emit.plain(v, col0 + j);
+                    } else {
+                        emit.ahead(res, col0 + j);
+                        emit(v, res, col0 + j);
+                    }
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) ptx::cluster_sync();  // neither CTA leaves while the other may signal or read it
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_cg<CG>(tmem, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------- the parts --
+
+// D[m, n] = sum of the parts (in order), then the epilogue. Four columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) reduce_kernel(const float* __restrict__ part, int splits, long long stride, int M,
+                                                     int N, int pitch, const T* __restrict__ bias,
+                                                     const T* residual, T* y, T* z, int act) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n4 = (N + 3) / 4;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)M * n4; i += gridDim.x * 256LL) {
+        const long long m = i / n4;
+        const int n = (int)(i - m * n4) * 4;
+        const float* p = part + m * pitch + n;
+        float v[4] = {};
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+            const float4 q = *reinterpret_cast<const float4*>(p + s * stride);
+            v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (n + c < N) {
+                const long long at = m * N + n + c;
+                float s = v[c];
+                if (bias) s += ld1(bias + n + c);
+                if (residual) s += ld1(residual + at);
+                if (z) z[at] = from_float<T>(s);
+                y[at] = from_float<T>(act_run(s, act));
+            }
+    }
+}
+
+// ----------------------------------------------------- operand preparation --
+
+// The three bfloat16 terms of v. The first is kept finite for a finite v, the others are zero
+// for an infinite or NaN v.
+__device__ __forceinline__ void split3(float v, bf16 (&t)[3]) {
+    const float top = 3.3895313892515355e38f;  // the largest bfloat16
+    const bool fin = fabsf(v) <= 3.4028234663852886e38f;
+    t[0] = __float2bfloat16_rn(fin ? fminf(fmaxf(v, -top), top) : v);
+    const float r1 = fin ? v - __bfloat162float(t[0]) : 0.f;
+    t[1] = __float2bfloat16_rn(r1);
+    t[2] = __float2bfloat16_rn(r1 - __bfloat162float(t[1]));
+}
+
+// out[term][r][c] (bfloat16, rows of `pitch`) = the terms of in[r][c]; eight columns a thread.
+template <typename T, int TERMS>
+__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ in, int rows, int cols, int pitch,
+                                                   bf16* __restrict__ out) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c8 = pitch / 8;
+    const long long plane = (long long)rows * pitch;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)rows * c8; i += gridDim.x * 256LL) {
+        const long long r = i / c8;
+        const int c = (int)(i - r * c8) * 8;
+        bf16 t[TERMS][8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float v = c + q < cols ? ld1(in + r * cols + c + q) : 0.f;
+            if constexpr (TERMS == 1) {
+                t[0][q] = __float2bfloat16_rn(v);
+            } else {
+                bf16 s[3];
+                split3(v, s);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) t[k][q] = s[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+            *reinterpret_cast<uint4*>(out + k * plane + r * pitch + c) = *reinterpret_cast<uint4*>(t[k]);
+    }
+}
+
+// dz = grad_y act'(saved): its bfloat16 terms (out, as pack_kernel; may be null), grad_residual (may be null), and
+// the column sums of a block's rows (sums[block][pitch]; may be null). A thread keeps eight columns and walks the
+// block's rows.
+template <typename T, int TERMS>
+__global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const T* __restrict__ saved, int act, int M,
+                                                 int N, int pitch, int rows, int cblocks, bf16* __restrict__ out,
+                                                 T* __restrict__ gr, float* __restrict__ sums) {
+    __shared__ float sm[256 * 8];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c8 = pitch / 8;
+    const int tx = min(c8, 256), ty = 256 / tx;
+    const int cx = threadIdx.x % tx, ry = threadIdx.x / tx;
+    const int rb = blockIdx.x / cblocks;
+    const int c = ((blockIdx.x % cblocks) * tx + cx) * 8;
+    const long long plane = (long long)M * pitch;
+    const int m0 = rb * rows, m1 = min(m0 + rows, M);
+    float sum[8] = {};
+    if (c < pitch && ry < ty) {
+        for (long long m = m0 + ry; m < m1; m += ty) {
+            bf16 t[TERMS][8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                float v = 0.f;
+                if (c + q < N) {
+                    v = ld1(gy + m * N + c + q);
+                    if (act != kActNone) {
+                        const float s = ld1(saved + m * N + c + q);
+                        v = act == kActRelu ? act_grad<kActRelu>(v, s)
+                                            : v * (act == kActSilu ? act_slope<kActSilu>(s) : act_slope<kActGelu>(s));
+                    }
+                    if (gr) gr[m * N + c + q] = from_float<T>(v);
+                }
+                sum[q] += v;
+                if constexpr (TERMS == 1) {
+                    t[0][q] = __float2bfloat16_rn(v);
+                } else {
+                    bf16 s[3];
+                    split3(v, s);
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) t[k][q] = s[k];
+                }
+            }
+            if (out)
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+                    *reinterpret_cast<uint4*>(out + k * plane + m * pitch + c) = *reinterpret_cast<uint4*>(t[k]);
+        }
+    }
+    if (!sums) return;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sm[threadIdx.x * 8 + q] = sum[q];
+    __syncthreads();
+    if (ry == 0 && c < pitch) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float v = 0.f;
+            for (int r = 0; r < ty; ++r) v += sm[(r * tx + cx) * 8 + q];
+            sums[(long long)rb * pitch + c + q] = v;
+        }
+    }
+}
+
+// grad_bias[n] = sum over the row blocks (32 columns, 8 lanes a block)
+__global__ void __launch_bounds__(256) bias_kernel(const float* __restrict__ sums, int blocks, int pitch, int N,
+                                                   float* __restrict__ gb) {
+    __shared__ float sm[8][33];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int q = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + q;
+    float v = 0.f;
+    if (n < N)
+        for (int i = l; i < blocks; i += 8) v += sums[(long long)i * pitch + n];
+    sm[l][q] = v;
+    __syncthreads();
+    if (l == 0 && n < N) {
+        for (int i = 1; i < 8; ++i) v += sm[i][q];
+        gb[n] = v;
+    }
+}
+
+// ------------------------------------------------------------------- host --
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// A bfloat16 matrix in memory, [terms][rows][pitch]: 16-byte aligned, pitch a multiple of 8.
+struct Matrix {
+    const void* p;
+    int rows, cols, pitch, terms;
+};
+
+// Its tensor map with boxes of 64 columns and `box` rows.
+bool encode(CUtensorMap* m, const Matrix& x, int box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)x.terms};
+    cuuint64_t strides[2] = {(cuuint64_t)x.pitch * 2, (cuuint64_t)x.pitch * 2 * x.rows};
+    cuuint32_t b[3] = {64, (cuuint32_t)box, 1}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... P, typename... Q>
+cudaError_t launch(void (*f)(P...), int grid, int threads, uint32_t smem, int cluster, cudaStream_t st, Q... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, f, P(args)...);
+}
+
+// How one product runs.
+struct GemmPlan {
+    bool swap;  // D's columns on the lanes
+    int cg, bn, splits, chunk;
+};
+
+// The cheapest of the tilings by a model of one CTA's cycles: per stage the larger of the MMAs (128 x 64 x bn at
+// 4096 a cycle, for each product of terms) and the operands' bytes from L2 (56 a cycle measured), per tile the
+// result's bytes (24 a cycle, an SM's share of HBM), and the parts' way through L2 where the reduction is split.
+GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool f32_out, int out_bytes) {
+    const int kblocks = (red + BK - 1) / BK;
+    const int sms = num_sms();
+    const int prods = ta == 1 ? 1 : tb == 1 ? 3 : 6;
+    GemmPlan best = {};
+    double best_t = 1e300;
+    for (int swap = 0; swap < 2; ++swap) {
+        const long long r = swap ? cols : rows, c = swap ? rows : cols;
+        const int sa = swap ? tb : ta, sb = swap ? ta : tb;
+        if (sa < sb) continue;  // the kernel takes the split operand as A
+        for (int cg = 1; cg <= 2; ++cg)
+            for (int bn = 64; bn <= (prods > 1 ? 128 : 256); bn *= 2) {
+                if (cg == 2 && bn < 128) continue;
+                if (bn > 64 && bn / 2 >= c) continue;
+                const long long mt = (r + BM * cg - 1) / (BM * cg), nt = (c + bn - 1) / bn;
+                const int slots = sms / cg;
+                const double stage = std::max(2.0 * bn * prods, (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
+                const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * out_bytes / 24.0;
+                for (int splits = 1; splits <= std::min(kblocks, 64); ++splits) {
+                    const long long units = mt * nt * splits;
+                    if (splits > 1 && units > slots) break;
+                    const long long waves = (units + slots - 1) / slots;
+                    const int kb = (kblocks + splits - 1) / splits;
+                    double t = waves * std::max(kb * stage, splits > 1 ? BM * bn * 4 / 40.0 : epi) +
+                               (splits > 1 ? BM * bn * 4 / 40.0 : epi) + 2000.0;
+                    if (splits > 1)
+                        t += 2500.0 + (double)rows * cols * (4.0 * splits + out_bytes) / (sms * 40.0);
+                    if (t < best_t) {
+                        best_t = t;
+                        best = {swap != 0, cg, bn, splits, 0};
+                    }
+                }
+            }
+    }
+    // float32 results: the accumulator is taken out every 256 (terms: 128) elements
+    best.chunk = f32_out ? (prods > 1 ? 2 : 4) : 1 << 28;
+    return best;
+}
+
+template <typename T, int PB, int CG>
+cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int grid, uint32_t smem,
+                        cudaStream_t st) {
+    static DeviceFlags attr;
+    cudaError_t e = max_dynamic_smem_once((const void*)gemm_tc_kernel<T, PB, CG>, SMEM_MAX, attr);
+    if (e != cudaSuccess) return e;
+    return launch(gemm_tc_kernel<T, PB, CG>, grid, THREADS, smem, CG, st, ma, mb, a);
+}
+
+template <typename T>
+struct Out {  // the result's epilogue
+    const T *bias, *residual;
+    T *y, *z;
+    int act;
+};
+
+size_t part_bytes(const GemmPlan& p, long long rows, long long cols) {
+    return p.splits > 1 ? (size_t)p.splits * rows * ((cols + 7) / 8 * 8) * 4 : 0;
+}
+
+// D [rows, cols] (rows of `cols`) = A B^T through the epilogue. A: K-major [rows, red], or (a_mn) [red, rows]; B alike
+// with cols. `parts`: room for the split reduction's results.
+template <typename T>
+cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix& B, bool b_mn, int rows, int cols,
+                     int red, const Out<T>& out, float* parts, bool f32_out, unsigned* status, cudaStream_t st,
+                     int* launches) {
+    const Matrix &L = p.swap ? B : A, &R = p.swap ? A : B;
+    const bool l_mn = p.swap ? b_mn : a_mn, r_mn = p.swap ? a_mn : b_mn;
+    GemmArgs a = {};
+    a.rows = p.swap ? cols : rows;
+    a.cols = p.swap ? rows : cols;
+    a.kblocks = (red + BK - 1) / BK;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.mt = (a.rows + BM * p.cg - 1) / (BM * p.cg);
+    a.nt = (a.cols + p.bn - 1) / p.bn;
+    a.bn = p.bn;
+    a.ta = L.terms;
+    a.tb = R.terms;
+    a.a_mn = l_mn;
+    a.b_mn = r_mn;
+    a.stage_bytes = L.terms * A_BYTES + R.terms * (uint32_t)(p.bn / p.cg) * 128;
+    a.stages = (int)std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 1024 - BAR_BYTES) / a.stage_bytes);
+    a.bar_off = a.stages * a.stage_bytes;
+    a.status = status;
+    const bool split = p.splits > 1;
+    const int pitch = split ? (cols + 7) / 8 * 8 : cols;
+    a.rs = p.swap ? 1 : pitch;
+    a.cs = p.swap ? pitch : 1;
+    a.part = (long long)rows * pitch;
+    if (split) {
+        a.y = parts;
+        a.vec = p.swap ? 0 : 2;
+    } else {
+        a.bias = out.bias;
+        a.residual = out.residual;
+        a.y = out.y;
+        a.z = out.z;
+        a.act = out.act;
+        const uintptr_t all = (uintptr_t)out.y | (uintptr_t)out.z | (uintptr_t)out.residual | (uintptr_t)(pitch * sizeof(T));
+        a.vec = p.swap ? 0 : all % 32 == 0 ? 2 : all % 16 == 0 ? 1 : 0;
+    }
+    CUtensorMap ma, mb;
+    if (!encode(&ma, L, l_mn ? BK : BM) || !encode(&mb, R, r_mn ? BK : p.bn / p.cg)) return cudaErrorInvalidValue;
+    const long long units = (long long)a.mt * a.nt * a.splits;
+    const int grid = (int)std::min<long long>(units, num_sms() / p.cg) * p.cg;
+    const uint32_t smem = a.bar_off + BAR_BYTES + 1024;
+    cudaError_t e;
+    auto go = [&](auto t, auto pb) {
+        using D = decltype(t);
+        constexpr int PB = decltype(pb)::value;
+        return p.cg == 2 ? launch_gemm<D, PB, 2>(ma, mb, a, grid, smem, st)
+                         : launch_gemm<D, PB, 1>(ma, mb, a, grid, smem, st);
+    };
+    if (f32_out) {
+        e = p.bn == 64    ? go(float{}, std::integral_constant<int, 64>{})
+            : p.bn == 128 ? go(float{}, std::integral_constant<int, 128>{})
+                          : go(float{}, std::integral_constant<int, 256>{});
+    } else if (split) {
+        e = go(float{}, std::integral_constant<int, 0>{});
+    } else {
+        e = go(T{}, std::integral_constant<int, 0>{});
+    }
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if (split) {
+        const long long n = ((long long)rows * ((cols + 3) / 4) + 255) / 256;
+        e = launch(reduce_kernel<T>, (int)std::min<long long>(n, num_sms() * 8), 256, 0, 1, st, (const float*)parts,
+                   p.splits, a.part, rows, cols, pitch, out.bias, out.residual, out.y, out.z, out.act);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    return cudaSuccess;
+}
+
+int up8(int v) { return (v + 7) / 8 * 8; }
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// What a call lays out in its workspace.
+struct FwdPlan {
+    bool pack_x, pack_w;
+    GemmPlan g;
+    size_t x, w, parts, total;
+};
+FwdPlan plan_forward(const LinearShape& s, int bf) {
+    FwdPlan p = {};
+    const int terms = bf ? 1 : 3;
+    bool xw, gy;
+    linear_tc_in_place(s, bf, &xw, &gy);
+    p.pack_x = p.pack_w = !xw;
+    p.g = plan_gemm(s.M, s.N, s.K, terms, terms, !bf, bf ? 2 : 4);
+    size_t o = 0;
+    p.x = o;
+    if (p.pack_x) o = up256(o + (size_t)terms * s.M * up8(s.K) * 2);
+    p.w = o;
+    if (p.pack_w) o = up256(o + (size_t)terms * s.N * up8(s.K) * 2);
+    p.parts = o;
+    p.total = o + part_bytes(p.g, s.M, s.N);
+    return p;
+}
+
+struct BwdPlan {
+    bool pack_x, pack_w, pass_dz;  // pass_dz: dz goes through the workspace
+    int dz_terms, tx, ty, cblocks, rblocks, rows;
+    GemmPlan gx, gw;
+    size_t x, w, dz, sums, parts, total;
+};
+BwdPlan plan_backward(const LinearShape& s, int bf) {
+    BwdPlan p = {};
+    const int terms = bf ? 1 : 3;
+    const bool smooth = s.act == kActSilu || s.act == kActGelu;
+    bool xw, gy;
+    linear_tc_in_place(s, bf, &xw, &gy);
+    p.pack_x = p.pack_w = !xw;
+    p.pass_dz = !gy;
+    // dz is exact in one bfloat16 term where it is grad_y or 0; grad_weight, a float32 result, takes three of the
+    // others
+    p.dz_terms = bf && !smooth ? 1 : 3;
+    // grad_x of a bfloat16 layer reads the first term alone: dz rounded once, as a grad_x in bfloat16 is
+    p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4);
+    p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4);
+    const int c8 = up8(s.N) / 8;
+    p.tx = std::min(c8, 256);
+    p.ty = 256 / p.tx;
+    p.cblocks = (c8 + p.tx - 1) / p.tx;
+    long long want = std::max(1, num_sms() * 4 / p.cblocks);
+    want = std::min<long long>(want, (s.M + 4LL * p.ty - 1) / (4LL * p.ty));
+    p.rows = (int)((s.M + want - 1) / want);
+    p.rblocks = (s.M + p.rows - 1) / p.rows;
+    size_t o = 0;
+    p.x = o;
+    if (p.pack_x) o = up256(o + (size_t)terms * s.M * up8(s.K) * 2);
+    p.w = o;
+    if (p.pack_w) o = up256(o + (size_t)terms * s.N * up8(s.K) * 2);
+    p.dz = o;
+    if (p.pass_dz) o = up256(o + (size_t)p.dz_terms * s.M * up8(s.N) * 2);
+    p.sums = o;
+    o = up256(o + (size_t)p.rblocks * up8(s.N) * 4);
+    p.parts = o;
+    p.total = o + std::max(part_bytes(p.gx, s.M, s.K), part_bytes(p.gw, s.N, s.K));
+    return p;
+}
+
+template <typename T>
+cudaError_t pack(const T* in, int rows, int cols, void* out, cudaStream_t st, int* launches) {
+    const int pitch = up8(cols);
+    const long long n = ((long long)rows * (pitch / 8) + 255) / 256;
+    ++*launches;
+    constexpr int TERMS = std::is_same<T, bf16>::value ? 1 : 3;
+    return launch(pack_kernel<T, TERMS>, (int)std::min<long long>(n, num_sms() * 16), 256, 0, 1, st, in, rows, cols,
+                  pitch, (bf16*)out);
+}
+
+template <typename T>
+cudaError_t forward_t(const LinearShape& s, const T* x, const T* w, const T* bias, const T* residual, T* y, T* z,
+                      uint8_t* ws, unsigned* status, cudaStream_t st, int* launches) {
+    constexpr int bf = std::is_same<T, bf16>::value;
+    const FwdPlan p = plan_forward(s, bf);
+    const int terms = bf ? 1 : 3;
+    Matrix X{x, s.M, s.K, s.K, 1}, W{w, s.N, s.K, s.K, 1};
+    cudaError_t e;
+    if (p.pack_x) {
+        if ((e = pack(x, s.M, s.K, ws + p.x, st, launches)) != cudaSuccess) return e;
+        X = {ws + p.x, s.M, s.K, up8(s.K), terms};
+    }
+    if (p.pack_w) {
+        if ((e = pack(w, s.N, s.K, ws + p.w, st, launches)) != cudaSuccess) return e;
+        W = {ws + p.w, s.N, s.K, up8(s.K), terms};
+    }
+    return run_gemm<T>(p.g, X, false, W, false, s.M, s.N, s.K, Out<T>{bias, residual, y, z, s.act},
+                       (float*)(ws + p.parts), !bf, status, st, launches);
+}
+
+template <typename T>
+cudaError_t backward_t(const LinearShape& s, const T* x, const T* w, const T* saved, const T* gy, T* gx, float* gw,
+                       float* gb, T* gr, uint8_t* ws, unsigned* status, cudaStream_t st, int* launches) {
+    constexpr int bf = std::is_same<T, bf16>::value;
+    const BwdPlan p = plan_backward(s, bf);
+    const int terms = bf ? 1 : 3;
+    cudaError_t e;
+    Matrix X{x, s.M, s.K, s.K, 1}, W{w, s.N, s.K, s.K, 1}, DZ{gy, s.M, s.N, s.N, 1};
+    const bool need_dz = gx || gw;
+    bf16* dz = p.pass_dz && need_dz ? (bf16*)(ws + p.dz) : nullptr;
+    if (dz || gb || gr) {
+        auto f = dz_kernel<T, 3>;
+        if constexpr (bf) {
+            if (p.dz_terms == 1) f = dz_kernel<T, 1>;
+        }
+        e = launch(f, p.rblocks * p.cblocks, 256, 0, 1, st, gy, saved, s.act, s.M, s.N, up8(s.N), p.rows, p.cblocks, dz,
+                   gr, gb ? (float*)(ws + p.sums) : nullptr);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        if (dz) DZ = {dz, s.M, s.N, up8(s.N), p.dz_terms};
+    }
+    if (gb) {
+        e = launch(bias_kernel, (s.N + 31) / 32, 256, 0, 1, st, (const float*)(ws + p.sums), p.rblocks, up8(s.N), s.N,
+                   gb);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    if (gx) {
+        if (p.pack_w) {
+            if ((e = pack(w, s.N, s.K, ws + p.w, st, launches)) != cudaSuccess) return e;
+            W = {ws + p.w, s.N, s.K, up8(s.K), terms};
+        }
+        Matrix first = DZ;
+        first.terms = terms;
+        e = run_gemm<T>(p.gx, first, false, W, true, s.M, s.K, s.N, Out<T>{nullptr, nullptr, gx, nullptr, kActNone},
+                        (float*)(ws + p.parts), !bf, status, st, launches);
+        if (e != cudaSuccess) return e;
+    }
+    if (gw) {
+        if (p.pack_x) {
+            if ((e = pack(x, s.M, s.K, ws + p.x, st, launches)) != cudaSuccess) return e;
+            X = {ws + p.x, s.M, s.K, up8(s.K), terms};
+        }
+        e = run_gemm<float>(p.gw, DZ, true, X, true, s.N, s.K, s.M, Out<float>{nullptr, nullptr, gw, nullptr, kActNone},
+                            (float*)(ws + p.parts), true, status, st, launches);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+void linear_tc_in_place(const LinearShape& s, int bf, bool* in_xw, bool* in_gy) {
+    *in_xw = bf && s.K % 8 == 0;
+    *in_gy = bf && s.N % 8 == 0 && s.act == kActNone;
+}
+
+size_t linear_tc_workspace(const LinearShape& s, int bf, bool backward) {
+    return backward ? plan_backward(s, bf).total : plan_forward(s, bf).total;
+}
+
+cudaError_t linear_tc_forward(const LinearShape& s, int bf, const void* x, const void* w, const void* bias,
+                              const void* residual, void* y, void* z, void* ws, unsigned* status, cudaStream_t st,
+                              int* launches) {
+    if (bf)
+        return forward_t(s, (const bf16*)x, (const bf16*)w, (const bf16*)bias, (const bf16*)residual, (bf16*)y,
+                         (bf16*)z, (uint8_t*)ws, status, st, launches);
+    return forward_t(s, (const float*)x, (const float*)w, (const float*)bias, (const float*)residual, (float*)y,
+                     (float*)z, (uint8_t*)ws, status, st, launches);
+}
+
+cudaError_t linear_tc_backward(const LinearShape& s, int bf, const void* x, const void* w, const void* saved,
+                               const void* gy, void* gx, float* gw, float* gb, void* gr, void* ws, unsigned* status,
+                               cudaStream_t st, int* launches) {
+    if (bf)
+        return backward_t(s, (const bf16*)x, (const bf16*)w, (const bf16*)saved, (const bf16*)gy, (bf16*)gx, gw, gb,
+                          (bf16*)gr, (uint8_t*)ws, status, st, launches);
+    return backward_t(s, (const float*)x, (const float*)w, (const float*)saved, (const float*)gy, (float*)gx, gw, gb,
+                      (float*)gr, (uint8_t*)ws, status, st, launches);
+}
+
+}  // namespace dcn

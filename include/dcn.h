@@ -267,7 +267,7 @@ typedef struct {
     unsigned flags;  /* DCN_FLAG_GENERIC or 0 */
 } dcn_linear_params_t;
 
-/* Bytes of workspace (16-byte aligned) of the forward (op DCN_OP_FORWARD) or the
+/* Bytes of workspace (256-byte aligned) of the forward (op DCN_OP_FORWARD) or the
  * backward (DCN_OP_BACKWARD); 0 when none is needed or params are invalid. */
 DCN_API size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op);
 
