@@ -21,7 +21,9 @@ parameter gradients are float32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -51,6 +53,7 @@ DCN_FLAG_GENERIC = 0x1
 DCN_FLAG_NO_TF32 = 0x2
 DCN_ERR_TIMEOUT, DCN_ERR_RANGE = -4, -6
 OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BACKWARD = 0, 1, 2, 3
+_MOST = 2 ** 31 - 1  # elements of a tensor that the library indexes
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 _DTYPES = {torch.float32: DCN_F32, torch.bfloat16: DCN_BF16}
 
@@ -345,31 +348,79 @@ def _activation(activation):
 
 
 def _check_shape(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _scratch(n, device, workspace):
-    """(tensor, bytes) of a workspace of at least n bytes: the caller's, or a new one."""
-    if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    return (torch.empty(n, dtype=torch.uint8, device=device), n) if n else (None, 0)
+def _check_like(like, shapes, /, **ts):
+    """Each tensor that is not None is contiguous, of the device and dtype of `like`, and of its shape in `shapes`."""
+    dtype, device = like.dtype, like.device
+    for name, t in ts.items():
+        if t is not None and (t.dtype is not dtype or t.device != device or not t.is_contiguous()
+                              or t.shape != shapes[name]):
+            _check_tensors(dtype, device, **{name: t})
+            _check_shape(name, t, shapes[name])
 
 
-def _linear_params(x, weight, activation, generic):
-    """(params, shape of y) for x [..., K] and weight [N, K] or [N, 1, 1, K]."""
-    if x.dim() < 1 or weight.dim() not in (2, 4) or weight.dim() == 4 and tuple(weight.shape[1:3]) != (1, 1):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(n, x, workspace):
+    """(tensor, address, bytes) of a workspace: the caller's, or a new one of n bytes."""
+    if workspace is None:
+        if not n:
+            return None, None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        return workspace, workspace.data_ptr(), n
+    if workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on %s" % x.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(fn, x, *args):
+    """fn(*args, stream) on x's device and its current stream."""
+    index = x.device.index
+    if index == torch._C._cuda_getDevice():
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
+def _on_device(x):
+    """The context in which sizes that depend on the device are asked for: x's device."""
+    return contextlib.nullcontext() if x.device.index == torch._C._cuda_getDevice() else torch.cuda.device(x.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_sizes(index, *fields):
+    """(params by reference, forward's and backward's workspace bytes) on the current device, number `index`."""
+    p = LinearParams(*fields)
+    return ctypes.byref(p), linear_workspace_size(p, OP_FORWARD), linear_workspace_size(p, OP_BACKWARD)
+
+
+def _linear_plan(x, weight, activation, generic):
+    """(_linear_sizes, y's shape, N) for x [..., K] and weight [N, K] or [N, 1, 1, K]."""
+    ws, xs = weight.shape, x.shape
+    if len(xs) < 1 or len(ws) not in (2, 4) or len(ws) == 4 and (ws[1] != 1 or ws[2] != 1):
         raise ValueError("x must be [..., K] and weight [N, K] or [N, 1, 1, K]")
     if x.dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
-    N, K = weight.shape[0], weight.shape[-1]
-    if x.shape[-1] != K:
-        raise ValueError("x must be [..., %d] for weight %s, got %s" % (K, tuple(weight.shape), tuple(x.shape)))
+    N, K = ws[0], ws[-1]
+    if xs[-1] != K:
+        raise ValueError("x must be [..., %d] for weight %s, got %s" % (K, tuple(ws), tuple(xs)))
     if N < 1 or K < 1:
-        raise ValueError("weight must not be empty, got %s" % (tuple(weight.shape),))
-    p = LinearParams(x.numel() // K, N, K, _activation(activation), _DTYPES[x.dtype],
-                     DCN_FLAG_GENERIC if generic else 0)
-    return p, (*x.shape[:-1], N)
+        raise ValueError("weight must not be empty, got %s" % (tuple(ws),))
+    act = _activation(activation)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor, got %s" % x.device)
+    if x.numel() > _MOST or weight.numel() > _MOST:
+        raise ValueError("a tensor exceeds 2^31-1 elements")
+    with _on_device(x):
+        sizes = _linear_sizes(x.device.index, x.numel() // K, N, K, act, _DTYPES[x.dtype],
+                              DCN_FLAG_GENERIC if generic else 0)
+    return sizes, xs[:-1] + (N,), N
 
 
 def linear_workspace_size(p: LinearParams, op: int) -> int:
@@ -383,17 +434,14 @@ def linear_forward(x, weight, bias=None, residual=None, activation="none", *, ne
     "relu", "silu" or "gelu" (with erf). need_preact: (y, z) with the pre-activation z, which the backward pass
     of silu and gelu takes. out: y to write; it may be the residual."""
     lib = _load()
-    p, shape = _linear_params(x, weight, activation, generic)
-    _check_tensors(x.dtype, x.device, x=x, weight=weight, bias=bias, residual=residual, out=out)
-    _check_shape("bias", bias, (p.N,))
-    _check_shape("residual", residual, shape)
-    _check_shape("out", out, shape)
-    with torch.cuda.device(x.device):
-        y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
-        z = torch.empty(shape, dtype=x.dtype, device=x.device) if need_preact else None
-        ws, nws = _scratch(linear_workspace_size(p, OP_FORWARD), x.device, workspace)
-        _check(lib.dcn_linear_forward(ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y),
-                                      _ptr(z), _ptr(ws), nws, _stream(x.device)))
+    (p, n, _), shape, N = _linear_plan(x, weight, activation, generic)
+    _check_like(x, {"x": x.shape, "weight": weight.shape, "bias": (N,), "residual": shape, "out": shape}, x=x,
+                weight=weight, bias=bias, residual=residual, out=out)
+    y = x.new_empty(shape) if out is None else out
+    z = x.new_empty(shape) if need_preact else None
+    ws, wp, n = _scratch(n, x, workspace)
+    _call(lib.dcn_linear_forward, x, p, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(residual), y.data_ptr(),
+          _addr(z), wp, n)
     return (y, z) if need_preact else y
 
 
@@ -403,33 +451,42 @@ def linear_backward(x, weight, saved, grad_y, activation="none", *, need_input=T
     the forward left, y for relu, the pre-activation z for silu and gelu, None for none. grad_x and
     grad_residual have x's dtype, grad_weight (weight's shape) and grad_bias are float32."""
     lib = _load()
-    p, shape = _linear_params(x, weight, activation, generic)
     if (saved is None) != (activation == "none"):
         raise ValueError("saved must be %s for activation %r" % (
             "None" if activation == "none" else "the output" if activation == "relu" else "the pre-activation",
             activation))
-    _check_tensors(x.dtype, x.device, x=x, weight=weight, saved=saved, grad_y=grad_y)
-    _check_shape("saved", saved, shape)
-    _check_shape("grad_y", grad_y, shape)
-    with torch.cuda.device(x.device):
-        f32 = dict(dtype=torch.float32, device=x.device)
-        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_input else None
-        gw = torch.empty(weight.shape, **f32) if need_weight else None
-        gb = torch.empty((p.N,), **f32) if need_bias else None
-        gr = torch.empty(shape, dtype=x.dtype, device=x.device) if need_residual else None
-        ws, nws = _scratch(linear_workspace_size(p, OP_BACKWARD), x.device, workspace)
-        _check(lib.dcn_linear_backward(ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(saved), _ptr(grad_y), _ptr(gx),
-                                       _ptr(gw), _ptr(gb), _ptr(gr), _ptr(ws), nws, _stream(x.device)))
+    (p, _, n), shape, N = _linear_plan(x, weight, activation, generic)
+    _check_like(x, {"x": x.shape, "weight": weight.shape, "saved": shape, "grad_y": shape}, x=x, weight=weight,
+                saved=saved, grad_y=grad_y)
+    gx = torch.empty_like(x) if need_input else None
+    gw = torch.empty_like(weight, dtype=torch.float32) if need_weight else None
+    gb = x.new_empty((N,), dtype=torch.float32) if need_bias else None
+    gr = torch.empty_like(grad_y) if need_residual else None
+    ws, wp, n = _scratch(n, x, workspace)
+    _call(lib.dcn_linear_backward, x, p, x.data_ptr(), weight.data_ptr(), _addr(saved), grad_y.data_ptr(), _addr(gx),
+          _addr(gw), _addr(gb), _addr(gr), wp, n)
     return gx, gw, gb, gr
 
 
-def _norm_params(x, groups, eps, activation):
+@functools.lru_cache(maxsize=1024)
+def _norm_sizes(index, *fields):
+    """(params by reference, forward's and backward's workspace bytes) on the current device, number `index`."""
+    p = NormParams(*fields)
+    return ctypes.byref(p), group_norm_workspace_size(p, OP_FORWARD), group_norm_workspace_size(p, OP_BACKWARD)
+
+
+def _norm_plan(x, groups, eps, activation):
     if x.dim() != 4:
         raise ValueError("x must be [B, H, W, C]")
     if x.dtype not in _DTYPES:
         raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
-    B, H, W, C = x.shape
-    return NormParams(B, H, W, C, int(groups), float(eps), _activation(activation), _DTYPES[x.dtype], 0)
+    act = _activation(activation)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor, got %s" % x.device)
+    if x.numel() > _MOST:
+        raise ValueError("a tensor exceeds 2^31-1 elements")
+    with _on_device(x):
+        return _norm_sizes(x.device.index, *x.shape, int(groups), float(eps), act, _DTYPES[x.dtype], 0)
 
 
 def group_norm_workspace_size(p: NormParams, op: int) -> int:
@@ -441,17 +498,15 @@ def group_norm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", *, o
     C / groups neighbouring channels, stats float32 [B, groups, 2] = (mean, rstd). gamma, beta [C] or None;
     activation as for linear_forward. out: y to write; it may be x."""
     lib = _load()
-    p = _norm_params(x, groups, eps, activation)
-    _check_tensors(x.dtype, x.device, x=x, gamma=gamma, beta=beta, out=out)
-    _check_shape("gamma", gamma, (p.C,))
-    _check_shape("beta", beta, (p.C,))
-    _check_shape("out", out, x.shape)
-    with torch.cuda.device(x.device):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        stats = torch.empty((p.B, max(p.groups, 0), 2), dtype=torch.float32, device=x.device)
-        ws, nws = _scratch(group_norm_workspace_size(p, OP_FORWARD), x.device, workspace)
-        _check(lib.dcn_group_norm_forward(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats),
-                                          _ptr(ws), nws, _stream(x.device)))
+    p, n, _ = _norm_plan(x, groups, eps, activation)
+    shape = x.shape
+    c = shape[3:]
+    _check_like(x, {"x": shape, "gamma": c, "beta": c, "out": shape}, x=x, gamma=gamma, beta=beta, out=out)
+    y = torch.empty_like(x) if out is None else out
+    stats = x.new_empty((shape[0], max(groups, 0), 2), dtype=torch.float32)
+    ws, wp, n = _scratch(n, x, workspace)
+    _call(lib.dcn_group_norm_forward, x, p, x.data_ptr(), _addr(gamma), _addr(beta), y.data_ptr(), stats.data_ptr(),
+          wp, n)
     return y, stats
 
 
@@ -460,22 +515,18 @@ def group_norm_backward(x, gamma, beta, stats, grad_y, groups, activation="none"
     """(grad_x, grad_gamma, grad_beta) of group_norm_forward, given its x and stats: grad_x in x's dtype,
     grad_gamma and grad_beta [C] float32, None where gamma or beta is None or not requested."""
     lib = _load()
-    p = _norm_params(x, groups, 1.0, activation)
-    _check_tensors(x.dtype, x.device, x=x, gamma=gamma, beta=beta, grad_y=grad_y)
+    p, _, n = _norm_plan(x, groups, 1.0, activation)
+    shape = x.shape
+    c = shape[3:]
+    _check_like(x, {"x": shape, "gamma": c, "beta": c, "grad_y": shape}, x=x, gamma=gamma, beta=beta, grad_y=grad_y)
     _check_tensors(torch.float32, x.device, stats=stats)
-    _check_shape("gamma", gamma, (p.C,))
-    _check_shape("beta", beta, (p.C,))
-    _check_shape("stats", stats, (p.B, p.groups, 2))
-    _check_shape("grad_y", grad_y, x.shape)
-    with torch.cuda.device(x.device):
-        f32 = dict(dtype=torch.float32, device=x.device)
-        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_input else None
-        gg = torch.empty((p.C,), **f32) if need_params and gamma is not None else None
-        gb = torch.empty((p.C,), **f32) if need_params and beta is not None else None
-        ws, nws = _scratch(group_norm_workspace_size(p, OP_BACKWARD), x.device, workspace)
-        _check(lib.dcn_group_norm_backward(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(stats),
-                                           _ptr(grad_y), _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws), nws,
-                                           _stream(x.device)))
+    _check_shape("stats", stats, (shape[0], groups, 2))
+    gx = torch.empty_like(x) if need_input else None
+    gg = x.new_empty(c, dtype=torch.float32) if need_params and gamma is not None else None
+    gb = x.new_empty(c, dtype=torch.float32) if need_params and beta is not None else None
+    ws, wp, n = _scratch(n, x, workspace)
+    _call(lib.dcn_group_norm_backward, x, p, x.data_ptr(), _addr(gamma), _addr(beta), stats.data_ptr(),
+          grad_y.data_ptr(), _addr(gx), _addr(gg), _addr(gb), wp, n)
     return gx, gg, gb
 
 

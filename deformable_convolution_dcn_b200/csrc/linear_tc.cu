@@ -492,8 +492,84 @@ __device__ __forceinline__ void split3(float v, bf16 (&t)[3]) {
     t[2] = __float2bfloat16_rn(r1 - __bfloat162float(t[1]));
 }
 
+// Eight values from p, `n` of them there (the others 0); VEC: all there, 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const float* p, int n) {
+    if constexpr (VEC) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < n ? ld1(p + q) : 0.f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const bf16* p, int n) {
+    if constexpr (VEC) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[2 * q] = __uint_as_float(w[q] << 16);
+            v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < n ? ld1(p + q) : 0.f;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+    return *reinterpret_cast<uint4*>(h);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
+    if constexpr (VEC) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < n) p[q] = v[q];
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(bf16* p, const float (&v)[8], int n) {
+    if constexpr (VEC) {
+        *reinterpret_cast<uint4*>(p) = pack8(v);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < n) p[q] = __float2bfloat16_rn(v[q]);
+    }
+}
+
+// The TERMS bfloat16 terms of eight values to out, out + plane, ...
+template <int TERMS>
+__device__ __forceinline__ void store_terms(bf16* out, long long plane, const float (&v)[8]) {
+    if constexpr (TERMS == 1) {
+        *reinterpret_cast<uint4*>(out) = pack8(v);
+    } else {
+        bf16 t[3][8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            bf16 s[3];
+            split3(v[q], s);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) t[k][q] = s[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(out + k * plane) = *reinterpret_cast<uint4*>(t[k]);
+    }
+}
+
 // out[term][r][c] (bfloat16, rows of `pitch`) = the terms of in[r][c]; eight columns a thread.
-template <typename T, int TERMS>
+// VEC: rows of `in` are whole vectors, 16-byte aligned.
+template <typename T, int TERMS, bool VEC>
 __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ in, int rows, int cols, int pitch,
                                                    bf16* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -503,31 +579,18 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ in, int
     for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)rows * c8; i += gridDim.x * 256LL) {
         const long long r = i / c8;
         const int c = (int)(i - r * c8) * 8;
-        bf16 t[TERMS][8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float v = c + q < cols ? ld1(in + r * cols + c + q) : 0.f;
-            if constexpr (TERMS == 1) {
-                t[0][q] = __float2bfloat16_rn(v);
-            } else {
-                bf16 s[3];
-                split3(v, s);
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k) t[k][q] = s[k];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-            *reinterpret_cast<uint4*>(out + k * plane + r * pitch + c) = *reinterpret_cast<uint4*>(t[k]);
+        float v[8];
+        load8<VEC>(v, in + r * cols + c, cols - c);
+        store_terms<TERMS>(out + r * pitch + c, plane, v);
     }
 }
 
 // dz = grad_y act'(saved): its bfloat16 terms (out, as pack_kernel; may be null), grad_residual (may be null), and
 // the column sums of a block's rows (sums[block][pitch]; may be null). A thread keeps eight columns and walks the
-// block's rows.
-template <typename T, int TERMS>
-__global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const T* __restrict__ saved, int act, int M,
-                                                 int N, int pitch, int rows, int cblocks, bf16* __restrict__ out,
+// block's rows. VEC as for pack_kernel, for gy, saved and gr.
+template <typename T, int ACT, int TERMS, bool VEC>
+__global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const T* __restrict__ saved, int M, int N,
+                                                 int pitch, int rows, int cblocks, bf16* __restrict__ out,
                                                  T* __restrict__ gr, float* __restrict__ sums) {
     __shared__ float sm[256 * 8];
     asm volatile("griddepcontrol.launch_dependents;");
@@ -541,34 +604,21 @@ __global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const
     const int m0 = rb * rows, m1 = min(m0 + rows, M);
     float sum[8] = {};
     if (c < pitch && ry < ty) {
+#pragma unroll 4
         for (long long m = m0 + ry; m < m1; m += ty) {
-            bf16 t[TERMS][8];
+            const long long at = m * N + c;
+            float v[8];
+            load8<VEC>(v, gy + at, N - c);
+            if constexpr (ACT != kActNone) {
+                float s[8];
+                load8<VEC>(s, saved + at, N - c);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                float v = 0.f;
-                if (c + q < N) {
-                    v = ld1(gy + m * N + c + q);
-                    if (act != kActNone) {
-                        const float s = ld1(saved + m * N + c + q);
-                        v = act == kActRelu ? act_grad<kActRelu>(v, s)
-                                            : v * (act == kActSilu ? act_slope<kActSilu>(s) : act_slope<kActGelu>(s));
-                    }
-                    if (gr) gr[m * N + c + q] = from_float<T>(v);
-                }
-                sum[q] += v;
-                if constexpr (TERMS == 1) {
-                    t[0][q] = __float2bfloat16_rn(v);
-                } else {
-                    bf16 s[3];
-                    split3(v, s);
-#pragma unroll
-                    for (int k = 0; k < TERMS; ++k) t[k][q] = s[k];
-                }
+                for (int q = 0; q < 8; ++q) v[q] = act_grad<ACT>(v[q], s[q]);
             }
-            if (out)
 #pragma unroll
-                for (int k = 0; k < TERMS; ++k)
-                    *reinterpret_cast<uint4*>(out + k * plane + m * pitch + c) = *reinterpret_cast<uint4*>(t[k]);
+            for (int q = 0; q < 8; ++q) sum[q] += v[q];
+            if (gr) store8<VEC>(gr + at, v, N - c);
+            if (out) store_terms<TERMS>(out + m * pitch + c, plane, v);
         }
     }
     if (!sums) return;
@@ -681,9 +731,13 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
                 const int slots = sms / cg;
                 const double stage = std::max(2.0 * bn * prods, (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
                 const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * out_bytes / 24.0;
-                for (int splits = 1; splits <= std::min(kblocks, 64); ++splits) {
+                // no split, or as many parts as fill the GPU once, or half of them
+                const int fill = (int)std::min<long long>(kblocks, std::max<long long>(1, slots / (mt * nt)));
+                int last = 0;
+                for (const int splits : {1, fill / 2, fill}) {
+                    if (splits <= last) continue;
+                    last = splits;
                     const long long units = mt * nt * splits;
-                    if (splits > 1 && units > slots) break;
                     const long long waves = (units + slots - 1) / slots;
                     const int kb = (kblocks + splits - 1) / splits;
                     double t = waves * std::max(kb * stage, splits > 1 ? BM * bn * 4 / 40.0 : epi) +
@@ -871,8 +925,9 @@ cudaError_t pack(const T* in, int rows, int cols, void* out, cudaStream_t st, in
     const long long n = ((long long)rows * (pitch / 8) + 255) / 256;
     ++*launches;
     constexpr int TERMS = std::is_same<T, bf16>::value ? 1 : 3;
-    return launch(pack_kernel<T, TERMS>, (int)std::min<long long>(n, num_sms() * 16), 256, 0, 1, st, in, rows, cols,
-                  pitch, (bf16*)out);
+    const bool vec = cols % 8 == 0 && ((uintptr_t)in & 15) == 0;
+    return launch(vec ? pack_kernel<T, TERMS, true> : pack_kernel<T, TERMS, false>,
+                  (int)std::min<long long>(n, num_sms() * 16), 256, 0, 1, st, in, rows, cols, pitch, (bf16*)out);
 }
 
 template <typename T>
@@ -906,12 +961,15 @@ cudaError_t backward_t(const LinearShape& s, const T* x, const T* w, const T* sa
     const bool need_dz = gx || gw;
     bf16* dz = p.pass_dz && need_dz ? (bf16*)(ws + p.dz) : nullptr;
     if (dz || gb || gr) {
-        auto f = dz_kernel<T, 3>;
-        if constexpr (bf) {
-            if (p.dz_terms == 1) f = dz_kernel<T, 1>;
-        }
-        e = launch(f, p.rblocks * p.cblocks, 256, 0, 1, st, gy, saved, s.act, s.M, s.N, up8(s.N), p.rows, p.cblocks, dz,
-                   gr, gb ? (float*)(ws + p.sums) : nullptr);
+        const bool vec = s.N % 8 == 0 && (((uintptr_t)gy | (uintptr_t)saved | (uintptr_t)gr) & 15) == 0;
+        e = with_act(s.act, [&](auto A) {
+            constexpr int ACT = decltype(A)::value;
+            // as BwdPlan::dz_terms
+            constexpr int TERMS = bf && (ACT == kActNone || ACT == kActRelu) ? 1 : 3;
+            return launch(vec ? dz_kernel<T, ACT, TERMS, true> : dz_kernel<T, ACT, TERMS, false>, p.rblocks * p.cblocks,
+                          256, 0, 1, st, gy, saved, s.M, s.N, up8(s.N), p.rows, p.cblocks, dz, gr,
+                          gb ? (float*)(ws + p.sums) : (float*)nullptr);
+        });
         if (e != cudaSuccess) return e;
         ++*launches;
         if (dz) DZ = {dz, s.M, s.N, up8(s.N), p.dz_terms};

@@ -211,7 +211,7 @@ def test_group_norm_refusals_on_the_device():
     with pytest.raises(ValueError, match="stats"):
         dcn.group_norm_backward(d["x"], None, None, torch.zeros(2, 3, 2, device="cuda"), d["gy"], 4)
     ws = torch.empty(8, dtype=torch.uint8, device="cuda")
-    p = dcn._norm_params(d["x"], 4, EPS, "none")
+    p = dcn.NormParams(2, 4, 4, 16, 4, EPS, 0, dcn.DCN_BF16, 0)
     if dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD) > 8:
         with pytest.raises(dcn.DcnError, match="workspace"):
             dcn.group_norm_backward(d["x"], None, None, given_stats(d, 4), d["gy"], 4, workspace=ws)
