@@ -19,35 +19,84 @@ __device__ __forceinline__ float ld1(const bf16* p) {
 // dcn_act_t values
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
 
-template <int ACT>
+// FAST: for values rounded to bfloat16 afterwards. Reciprocal and power of two are the hardware's approximations
+// (relative error below 2^-21), and the normal distribution's tail is the rational approximation of Abramowitz and
+// Stegun, formula 7.1.26 (absolute error 1.5e-7 of erf).
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ float sigmoid_fast(float z) { return rcp_fast(1.f + exp2_fast(z * -1.4426950408889634f)); }
+
+// e = exp(-z^2 / 2), tail = 1 - Phi(|z|)
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+    const float t = rcp_fast(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+    e = exp2_fast(z * z * (-0.5f * 1.4426950408889634f));
+    float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    p = fmaf(p, t, 0.5f * 1.421413741f);
+    p = fmaf(p, t, 0.5f * -0.284496736f);
+    p = fmaf(p, t, 0.5f * 0.254829592f);
+    return p * t * e;
+}
+
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act_apply(float z) {
-    if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // a NaN stays one
-    if constexpr (ACT == kActSilu) return z / (1.f + expf(-z));
-    if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == kActRelu) {
+        float r;
+        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));  // a NaN stays one
+        return r;
+    }
+    if constexpr (ACT == kActSilu) return FAST ? z * sigmoid_fast(z) : z / (1.f + expf(-z));
+    if constexpr (ACT == kActGelu) {
+        if constexpr (FAST) {
+            float e;
+            const float h = normal_tail(z, e);
+            const float zh = h == 0.f ? 0.f : fabsf(z) * h;  // an infinite z times an empty tail is 0
+            return fmaxf(z, 0.f) - zh;
+        }
+        return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    }
     return z;
 }
 
 // d act / dz. s is the pre-activation z; for relu its output serves as well
 // (both are positive at the same places).
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act_slope(float s) {
     if constexpr (ACT == kActRelu) return s > 0.f ? 1.f : 0.f;
     if constexpr (ACT == kActSilu) {
-        const float g = 1.f / (1.f + expf(-s));
+        const float g = FAST ? sigmoid_fast(s) : 1.f / (1.f + expf(-s));
         return g * (1.f + s * (1.f - g));
     }
-    if constexpr (ACT == kActGelu)
+    if constexpr (ACT == kActGelu) {
+        if constexpr (FAST) {
+            float e;
+            const float h = normal_tail(s, e);
+            return (s >= 0.f ? 1.f - h : h) + s * e * 0.39894228040143268f;
+        }
         return 0.5f * (1.f + erff(s * 0.70710678118654752f)) + s * expf(-0.5f * s * s) * 0.39894228040143268f;
+    }
     return 1.f;
 }
 
 // grad_z = grad_y * act'(s); relu selects, so that an infinite grad_y does not become NaN at slope 0
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act_grad(float gy, float s) {
     if constexpr (ACT == kActNone) return gy;
     if constexpr (ACT == kActRelu) return s > 0.f ? gy : 0.f;
-    return gy * act_slope<ACT>(s);
+    return gy * act_slope<ACT, FAST>(s);
 }
+
+// the kernels of a type: bfloat16 takes the fast functions
+template <typename T>
+constexpr bool kFast = std::is_same<T, bf16>::value;
 
 // Calls f(std::integral_constant<int, ACT>) for the run-time activation.
 template <typename F>

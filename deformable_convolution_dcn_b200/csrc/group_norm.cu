@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(NT) apply_kernel(const NormShape s, const Plan
         float v[V];
         load<T, V>(v, x + at + (size_t)r * s.C);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = act_apply<ACT>(fmaf(v[i] - mean[i], a[i], be[i]));
+        for (int i = 0; i < V; ++i) v[i] = act_apply<ACT, kFast<T>>(fmaf(v[i] - mean[i], a[i], be[i]));
         store<T, V>(y + at + (size_t)r * s.C, v);
     }
 }
@@ -266,7 +266,7 @@ __device__ __noinline__ bool positive64(float x, float mean, float rstd, float g
 }
 
 // dz of one value. hat = (x - mean) rstd.
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ float dz_of(float gy, float x, float hat, float mean, float rstd, float ga, float be) {
     const float z = fmaf(hat, ga, be);
     if constexpr (ACT == kActRelu) {
@@ -275,7 +275,7 @@ __device__ __forceinline__ float dz_of(float gy, float x, float hat, float mean,
             up = positive64(x, mean, rstd, ga, be);
         return up ? gy : 0.f;
     }
-    return act_grad<ACT>(gy, z);
+    return act_grad<ACT, FAST>(gy, z);
 }
 
 // sums[(b * chunks + chunk) * C + c] = (sum dz, sum dz xh) over the chunk's pixels
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NT) bwd_sums_kernel(const NormShape s, const P
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float hat = (v[i] - mean[i]) * rstd[i];
-                const float d = dz_of<ACT>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
+                const float d = dz_of<ACT, kFast<T>>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
                 s1[i] += d;
                 s2[i] = fmaf(d, hat, s2[i]);
             }
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(NT) bwd_apply_kernel(const NormShape s, const 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float hat = (v[i] - mean[i]) * rstd[i];
-            const float d = dz_of<ACT>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
+            const float d = dz_of<ACT, kFast<T>>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
             v[i] = rstd[i] * (fmaf(ga[i], d, -c1[i]) - hat * c2[i]);
         }
         store<T, V>(gx + at + (size_t)r * s.C, v);

@@ -31,7 +31,7 @@ struct Dz {  // dz(i, r), or transposed
         const long long at = i * si + r * sr;
         const float g = ld1(gy + at);
         if constexpr (ACT == kActNone) return g;
-        return act_grad<ACT>(g, ld1(saved + at));
+        return act_grad<ACT, false>(g, ld1(saved + at));
     }
 };
 
@@ -45,7 +45,7 @@ struct Epilogue {  // bias, residual, pre-activation, activation
         if (bias) v += ld1(bias + j);
         if (residual) v += ld1(residual + at);
         if (z) z[at] = from_float<T>(v);
-        y[at] = from_float<T>(act_apply<ACT>(v));
+        y[at] = from_float<T>(act_apply<ACT, false>(v));
     }
 };
 

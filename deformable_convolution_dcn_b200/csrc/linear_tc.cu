@@ -41,7 +41,9 @@ constexpr int THREADS = 64 + EPI_WARPS * 32;
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t A_BYTES = BM * BK * 2; // one term of one stage
 constexpr uint32_t MN_BLOCK = BK * 128;   // 64 rows of an MN-major operand over a stage: 8 KB
-constexpr uint32_t SMEM_MAX = 227 * 1024, BAR_BYTES = 256;
+constexpr int MAX_SLOTS = 3;
+constexpr uint32_t SMEM_MAX = 227 * 1024, BAR_BYTES = 512;
+constexpr uint32_t SLOT_BYTES = 4096, EXCHANGE_BYTES = 32 * 33 * 4, BIAS_BYTES = 128 * 4;  // a warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_LIMIT = 2000000000LL;
 
@@ -60,164 +62,215 @@ struct GemmArgs {
     const void *bias, *residual;
     void *y, *z;
     int act;
-    int vec;               // 2 / 1: rows of D are 32- / 16-byte aligned; 0: element by element
+    int tma_out;           // D's rows are 16-byte aligned and written as they lie: TMA stores
+    int nslots;            // chunks a warp stages (tma_out)
+    uint32_t slot_off, sm_off;  // the epilogue's slots or exchange buffers; its bias
     unsigned* status;
 };
 
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int mn, int k) {
-    // K-major: 16 reduction elements on = 32 bytes on; MN-major: 16 rows of 128 bytes on,
-    // blocks of 64 rows MN_BLOCK apart (leading byte offset)
-    uint64_t d = ptx::sw128_desc(addr + (mn ? k * 2048 : k * 32));
-    if (mn) d = (d & ~((uint64_t)0x3FFFu << 16)) | ((uint64_t)(MN_BLOCK >> 4) << 16);
-    return d;
-}
+// Shared-memory descriptors of one operand's tiles. Only the start address (the low word, in 16-byte units) changes
+// from one MMA to the next: by `step` for 16 reduction elements (K-major: 32 bytes on; MN-major: 16 rows of 128
+// bytes on, with blocks of 64 rows MN_BLOCK apart as leading byte offset).
+struct OperandDesc {
+    uint32_t low, high, step;
+    __device__ OperandDesc(uint32_t addr, int mn) {
+        uint64_t d = ptx::sw128_desc(addr);
+        if (mn) d = (d & ~((uint64_t)0x3FFFu << 16)) | ((uint64_t)(MN_BLOCK >> 4) << 16);
+        low = (uint32_t)d;
+        high = (uint32_t)(d >> 32);
+        step = mn ? 2048 / 16 : 32 / 16;
+    }
+    // k: steps, off: 16-byte units (no carry leaves the address field: shared memory ends below 2^18)
+    __device__ __forceinline__ uint64_t at(uint32_t off, int k) const {
+        return ((uint64_t)high << 32) | (low + off + k * step);
+    }
+};
 
+template <bool FAST>
 __device__ __forceinline__ float act_run(float z, int act) {
     switch (act) {
-        case kActRelu: return act_apply<kActRelu>(z);
-        case kActSilu: return act_apply<kActSilu>(z);
-        case kActGelu: return act_apply<kActGelu>(z);
+        case kActRelu: return act_apply<kActRelu, FAST>(z);
+        case kActSilu: return act_apply<kActSilu, FAST>(z);
+        case kActGelu: return act_apply<kActGelu, FAST>(z);
         default: return z;
     }
 }
 
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_apply<ACT>(v[i]);
+    for (int i = 0; i < 32; ++i) v[i] = act_apply<ACT, FAST>(v[i]);
 }
 
+// 16 bytes of a row of D: 8 bfloat16 or 4 float32 values.
 template <typename T>
-struct Pack32;  // 32 values of a row <-> 32-byte vectors
-template <>
-struct Pack32<float> {
-    static constexpr int N = 32;  // words
-    static __device__ __forceinline__ void put(uint32_t (&w)[32], const float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-    }
-    static __device__ __forceinline__ void add(float (&v)[32], const uint32_t (&w)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(w[i]);
-    }
-};
-template <>
-struct Pack32<bf16> {
-    static constexpr int N = 16;
-    static __device__ __forceinline__ void put(uint32_t (&w)[16], const float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
-    static __device__ __forceinline__ void add(float (&v)[32], const uint32_t (&w)[16]) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[2 * i] += __uint_as_float(w[i] << 16);
-            v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-};
-
-template <int N>
-__device__ __forceinline__ void load_row(uint32_t (&w)[N], const void* p, int vec) {
-    if (vec == 2) {
-#pragma unroll
-        for (int i = 0; i < N; i += 8)
-            ptx::ldg_v8(*reinterpret_cast<uint32_t(*)[8]>(&w[i]), static_cast<const char*>(p) + i * 4);
+constexpr int kVec = 16 / (int)sizeof(T);
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+    if constexpr (std::is_same<T, float>::value) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     } else {
+        __nv_bfloat162 h[4];
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                         : "l"(static_cast<const char*>(p) + i * 4));
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        return *reinterpret_cast<uint4*>(h);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void add16(float* v, uint4 w) {
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, float>::value) {
+            v[i] += __uint_as_float(q[i]);
+        } else {
+            v[2 * i] += __uint_as_float(q[i] << 16);
+            v[2 * i + 1] += __uint_as_float(q[i] & 0xFFFF0000u);
         }
     }
 }
-template <int N>
-__device__ __forceinline__ void store_row(void* p, const uint32_t (&w)[N], int vec) {
-    if (vec == 2) {
-#pragma unroll
-        for (int i = 0; i < N; i += 8)
-            ptx::stg_v8(static_cast<char*>(p) + i * 4, *reinterpret_cast<const uint32_t(*)[8]>(&w[i]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    }
-}
 
-// The epilogue of 32 columns of one row of D.
+// One warp's epilogue: 32 rows of D, one a lane, in chunks of 128 bytes a row. A chunk goes out through a 4 KB
+// shared-memory slot of the warp by a TMA store of its own (a lane writes 16-byte pieces of its row, 128-byte
+// swizzled: no bank conflicts, where direct stores would touch 32 lines an instruction), and the residual comes in
+// by TMA through the slots ahead, to be overwritten in place; no two warps wait for each other.
 template <typename T>
 struct Emit {
+    static constexpr int COLS = 128 / (int)sizeof(T);  // columns a chunk
     const GemmArgs& a;
+    const CUtensorMap *my, *mz, *mr;
     T *y, *z;
     const T *bias, *residual;
-    int row;
-    __device__ __forceinline__ bool whole(int col) const { return a.vec && row < a.rows && col + 32 <= a.cols; }
-    // residual values ahead of the accumulator
-    __device__ __forceinline__ void ahead(uint32_t (&r)[Pack32<T>::N], int col) const {
-        if (residual && whole(col)) load_row(r, residual + row * a.rs + col, a.vec);
-    }
-    __device__ __forceinline__ void plain(const float (&v)[32], int col) const {
-        if (whole(col)) {
-            uint32_t w[Pack32<T>::N];
-            Pack32<T>::put(w, v);
-            store_row(y + row * a.rs + col, w, a.vec);
-        } else if (row < a.rows) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col + i < a.cols) y[row * a.rs + (col + i) * a.cs] = from_float<T>(v[i]);
+    uint32_t slots, resbar;  // shared addresses of the warp's slots and of their residual barriers
+    float *sm, *sbias;       // exchange buffer (32 x 33), bias of the warp's columns
+    volatile int* abort;
+    int lane;
+    // the chunk's place
+    int row0, sp;
+    int out = 0;             // chunks written
+    int in = 0;              // residual chunks asked for
+    bool ok = true;
+
+    __device__ __forceinline__ bool active(int row, int col) const { return row < a.rows && col < a.cols; }
+    // the residual of one active chunk into its slot (the slot's last store has been read)
+    __device__ __forceinline__ void fetch(int row, int col) {
+        if (lane == 0) {
+            const int s = in % a.nslots;
+            ptx::mbar_arrive_expect_tx(resbar + s * 8, 4096);
+            ptx::tma_load_3d<1>(slots + s * 4096, mr, resbar + s * 8, col, row, 0);
         }
+        ++in;
     }
-    __device__ __forceinline__ void operator()(float (&v)[32], const uint32_t (&r)[Pack32<T>::N], int col) const {
-        if (bias) {
-            if (a.cs == 1) {  // bias by column: one coalesced load, spread by shuffles (all lanes are here)
-                const int c = col + (int)(threadIdx.x & 31);
-                const float b = c < a.cols ? ld1(bias + c) : 0.f;
+    // `v`: COLS columns from `col`, whose bias is sbias[b..]
+    __device__ __forceinline__ void chunk(float (&v)[COLS], int col, int b, bool epilogue) {
+        if (!a.tma_out) {
+            if (active(row0, col))
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(~0u, b, i);
-            } else {
-                const float b = row < a.rows ? ld1(bias + row) : 0.f;
+                for (int i = 0; i < COLS; i += 32)
+                    through_shared(*reinterpret_cast<float(*)[32]>(&v[i]), col + i);
+            return;
+        }
+        if (!active(row0, col)) return;
+        const int s = out % a.nslots;
+        const uint32_t slot = slots + s * 4096, mine = slot + lane * 128;
+        if (epilogue) {
+            if (bias) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += b;
+                for (int i = 0; i < COLS; i += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(sbias + b + i);
+                    v[i] += w.x, v[i + 1] += w.y, v[i + 2] += w.z, v[i + 3] += w.w;
+                }
+            }
+            if (residual) {
+                ok = ptx::mbar_wait(resbar + s * 8, (out / a.nslots) & 1, abort, a.status, WAIT_LIMIT) && ok;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    add16<T>(&v[i * kVec<T>], ptx::lds_v4(mine + ((i ^ (lane & 7)) << 4)));
             }
         }
-        if (whole(col)) {
-            const long long at = row * a.rs + col;
-            if (residual) Pack32<T>::add(v, r);
-            uint32_t w[Pack32<T>::N];
-            if (z) {
-                Pack32<T>::put(w, v);
-                store_row(z + at, w, a.vec);
-            }
+        // a slot is written again once the store before has read it (lane 0 issued it)
+        if (!residual && lane == 0) {
+            if (a.nslots == 2) ptx::bulk_wait_group_read<1>();
+            else ptx::bulk_wait_group_read<0>();
+        }
+        __syncwarp();
+        if (epilogue && z) {
+            put(v, mine);
+            send(mz, slot, col);
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+        }
+        if (epilogue) {
             switch (a.act) {
-                case kActRelu: act32<kActRelu>(v); break;
-                case kActSilu: act32<kActSilu>(v); break;
-                case kActGelu: act32<kActGelu>(v); break;
+                case kActRelu: act_all<kActRelu>(v); break;
+                case kActSilu: act_all<kActSilu>(v); break;
+                case kActGelu: act_all<kActGelu>(v); break;
                 default: break;
             }
-            Pack32<T>::put(w, v);
-            store_row(y + at, w, a.vec);
-        } else if (row < a.rows) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col + i < a.cols) {
-                    const long long at = row * a.rs + (col + i) * a.cs;
-                    float s = v[i];
-                    if (residual) s += ld1(residual + at);
-                    if (z) z[at] = from_float<T>(s);
-                    y[at] = from_float<T>(act_run(s, a.act));
-                }
         }
+        put(v, mine);
+        send(my, slot, col);
+        ++out;
+    }
+    // the slot of the chunk before has been read by its store: a residual chunk may be fetched into it
+    __device__ __forceinline__ void freed() {
+        if (lane == 0) ptx::bulk_wait_group_read<1>();
+        __syncwarp();
+    }
+    template <int ACT>
+    __device__ __forceinline__ void act_all(float (&v)[COLS]) {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) v[i] = act_apply<ACT, kFast<T>>(v[i]);
+    }
+    __device__ __forceinline__ void put(const float (&v)[COLS], uint32_t mine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ptx::sts_v4(mine + ((i ^ (lane & 7)) << 4), pack16<T>(&v[i * kVec<T>]));
+    }
+    __device__ __forceinline__ void send(const CUtensorMap* m, uint32_t slot, int col) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_3d(m, slot, col, row0, sp);
+            ptx::bulk_commit_group();
+        }
+    }
+    // Rows that are not whole vectors, and D written transposed: the values change lanes in shared memory, so that a
+    // warp's accesses lie side by side either way.
+    __device__ __forceinline__ void through_shared(const float (&v)[32], int col) {
+        if (col >= a.cols) return;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sm[lane * 33 + i] = v[i];
+        __syncwarp();
+        const bool rows_on_lanes = a.cs != 1;
+        const int mine = (rows_on_lanes ? row0 : col) + lane;  // this lane's row or column
+        const int n = min(32, rows_on_lanes ? a.cols - col : a.rows - row0);
+        if (mine < (rows_on_lanes ? a.rows : a.cols)) {
+            const float b = bias ? ld1(bias + mine) : 0.f;
+            long long at = rows_on_lanes ? mine + col * a.cs : row0 * a.rs + mine;
+            const long long step = rows_on_lanes ? a.cs : a.rs;
+            const float* p = rows_on_lanes ? sm + lane * 33 : sm + lane;
+            const int ps = rows_on_lanes ? 1 : 33;
+            T* yp = y + sp * a.part;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i, at += step) {
+                float s = p[i * ps] + b;
+                if (residual) s += ld1(residual + at);
+                if (z) z[at] = from_float<T>(s);
+                yp[at] = from_float<T>(act_run<kFast<T>>(s, a.act));
+            }
+        }
+        __syncwarp();
     }
 };
 
 // T: element type of D. PB: 0, or BN where the accumulator is added up in registers.
 template <typename T, int PB, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
-    gemm_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb, const GemmArgs a) {
+    gemm_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
+                   const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CUtensorMap tmz,
+                   const __grid_constant__ CUtensorMap tmr, const GemmArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -226,7 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.bar_off);
     const uint32_t full = ptx::smem_u32(bars), empty = full + MAX_STAGES * 8;
     const uint32_t accfull = empty + MAX_STAGES * 8, accempty = accfull + 16, done = accempty + 16;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 5);
+    const uint32_t resbar = done + 8;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 5 + EPI_WARPS * MAX_SLOTS);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     const uint32_t base = ptx::smem_u32(smem);
 
@@ -241,6 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ptx::mbar_init(accempty + i * 8, EPI_WARPS * CG);
         }
         ptx::mbar_init(done, 1);
+        for (int i = 0; i < EPI_WARPS * MAX_SLOTS; ++i) ptx::mbar_init(resbar + i * 8, 1);
         *s_abort = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tma);
@@ -269,20 +324,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             // ---- TMA producer: this CTA's rows of A, its share of B's rows
             const int bn = a.bn / CG;
-            int it = 0;
+            int stage = 0, it = 0;
+            uint32_t phase = 1;  // of the empty barrier: the first round of stages is free
             bool ok = true;
             for (int u = group; u < units && ok; u += groups) {
                 int im, in, k0, k1, sp;
                 unit_of(u, im, in, k0, k1, sp);
                 const int r0 = (im * CG + rank) * BM, c0 = in * a.bn + rank * bn;
                 for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = it % a.stages;
-                    if (it >= a.stages)
-                        ok = ptx::mbar_wait(empty + s * 8, ((it / a.stages) - 1) & 1, s_abort, a.status, WAIT_LIMIT);
+                    ok = ptx::mbar_wait(empty + stage * 8, phase, s_abort, a.status, WAIT_LIMIT);
                     if (!ok) break;
-                    const uint32_t bar = full + s * 8;
+                    const uint32_t bar = full + stage * 8;
                     if (rank == 0) ptx::mbar_arrive_expect_tx(bar, a.stage_bytes * CG);
-                    uint32_t dst = base + s * a.stage_bytes;
+                    uint32_t dst = base + stage * a.stage_bytes;
                     for (int t = 0; t < a.ta; ++t, dst += A_BYTES) {
                         if (a.a_mn) {
                             ptx::tma_load_3d<CG>(dst, &tma, bar, r0, kb * BK, t);
@@ -299,6 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             ptx::tma_load_3d<CG>(dst, &tmb, bar, kb * BK, c0, t);
                         }
                     }
+                    if (++stage == a.stages) stage = 0, phase ^= 1;
                 }
             }
             // copies still in flight land before the CTA may exit (bounded)
@@ -310,52 +365,62 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            // ---- MMA issue
+            // ---- MMA issue. The loop is one thread's serial work: it keeps nothing that needs a division or a
+            // 64-bit sum per step (with both, a stage took 850 cycles whatever its size; its MMAs take 2 bn)
             const uint32_t idesc =
                 ptx::idesc_bf16_f32(BM * CG, a.bn) | ((uint32_t)a.a_mn << 15) | ((uint32_t)a.b_mn << 16);
-            const uint32_t bterm = (uint32_t)(a.bn / CG) * 128;
-            int it = 0, ci = 0;
+            const OperandDesc da(base, a.a_mn), db(base + a.ta * A_BYTES, a.b_mn);
+            const uint32_t aterm = A_BYTES / 16, bterm = (uint32_t)(a.bn / CG) * 128 / 16;
+            const uint32_t stage_units = a.stage_bytes / 16;
+            const bool many = a.ta > 1, both = a.tb > 1;
+            int stage = 0;
+            uint32_t phase = 0, acc_phase = 1, off = 0;
+            int buf = 0;
             bool ok = true;
             for (int u = group; u < units && ok; u += groups) {
                 int im, in, k0, k1, sp;
                 unit_of(u, im, in, k0, k1, sp);
-                for (int c0 = k0; c0 < k1 && ok; c0 += a.chunk, ++ci) {
-                    const int buf = ci & 1;
-                    if (ci >= 2) {
-                        ok = ptx::mbar_wait(accempty + buf * 8, ((ci >> 1) - 1) & 1, s_abort, a.status, WAIT_LIMIT);
-                        if (!ok) break;
-                    }
+                for (int c0 = k0; c0 < k1 && ok; c0 += a.chunk) {
+                    ok = ptx::mbar_wait(accempty + buf * 8, acc_phase, s_abort, a.status, WAIT_LIMIT);
+                    if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t acc = tmem + buf * 256, low = acc + 128;
                     const int c1 = min(c0 + a.chunk, k1);
-                    for (int kb = c0; kb < c1; ++kb, ++it) {
-                        const int s = it % a.stages;
-                        ok = ptx::mbar_wait(full + s * 8, (it / a.stages) & 1, s_abort, a.status, WAIT_LIMIT);
+                    uint32_t more = 0;
+                    for (int kb = c0; kb < c1; ++kb) {
+                        ok = ptx::mbar_wait(full + stage * 8, phase, s_abort, a.status, WAIT_LIMIT);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        const uint32_t as = base + s * a.stage_bytes, bs = as + a.ta * A_BYTES;
+                        if (!many) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t a0 = operand_desc(as, a.a_mn, k), b0 = operand_desc(bs, a.b_mn, k);
-                            const uint32_t more = (kb > c0 || k > 0) ? 1u : 0u;
-                            ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
-                            if (a.ta > 1) {
-                                const uint64_t a1 = operand_desc(as + A_BYTES, a.a_mn, k);
-                                const uint64_t a2 = operand_desc(as + 2 * A_BYTES, a.a_mn, k);
-                                ptx::mma_bf16_cg<CG>(low, a2, b0, idesc, more);
+                            for (int k = 0; k < 4; ++k) {
+                                ptx::mma_bf16_cg<CG>(acc, da.at(off, k), db.at(off, k), idesc, more);
+                                more = 1;
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t a0 = da.at(off, k), b0 = db.at(off, k);
+                                ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
+                                ptx::mma_bf16_cg<CG>(low, da.at(off + 2 * aterm, k), b0, idesc, more);
+                                more = 1;
+                                const uint64_t a1 = da.at(off + aterm, k);
                                 ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, 1u);
-                                if (a.tb > 1) {
-                                    const uint64_t b1 = operand_desc(bs + bterm, a.b_mn, k);
-                                    const uint64_t b2 = operand_desc(bs + 2 * bterm, a.b_mn, k);
-                                    ptx::mma_bf16_cg<CG>(low, a0, b2, idesc, 1u);
+                                if (both) {
+                                    const uint64_t b1 = db.at(off + bterm, k);
+                                    ptx::mma_bf16_cg<CG>(low, a0, db.at(off + 2 * bterm, k), idesc, 1u);
                                     ptx::mma_bf16_cg<CG>(low, a1, b1, idesc, 1u);
                                     ptx::mma_bf16_cg<CG>(low, a0, b1, idesc, 1u);
                                 }
                             }
                         }
-                        ptx::mma_commit_cg<CG>(empty + s * 8);
+                        ptx::mma_commit_cg<CG>(empty + stage * 8);
+                        off += stage_units;
+                        if (++stage == a.stages) stage = 0, off = 0, phase ^= 1;
                     }
                     ptx::mma_commit_cg<CG>(accfull + buf * 8);
+                    buf ^= 1;
+                    acc_phase ^= buf ^ 1;
                 }
             }
             // every issued MMA has completed before TMEM and shared memory are released (bounded)
@@ -364,76 +429,139 @@ __global__ void __launch_bounds__(THREADS, 1)
             ptx::mbar_wait(done, 0, &none, a.status, WAIT_LIMIT);
         }
     } else {
-        // ---- epilogue: quarter q of the lanes, half h of the columns
-        const int q = warp & 3, h = (warp - 2) >> 2;
-        const int half = a.bn / 2;
+        // ---- epilogue: quarter q of the lanes, part h of the columns (a part is a whole chunk at least)
+        constexpr int COLS = Emit<T>::COLS;
+        const int w = warp - 2, q = warp & 3, h = w >> 2;
+        const int half = max(a.bn / 2, COLS), nch = h * half < a.bn ? half / COLS : 0;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + h * half;
-        int ci = 0;
-        bool ok = true;
-        for (int u = group; u < units && ok; u += groups) {
-            int im, in, k0, k1, sp;
+        int buf = 0;
+        uint32_t phase = 0;
+        Emit<T> emit{a, &tmy, &tmz, &tmr, (T*)a.y, (T*)a.z, (const T*)a.bias, (const T*)a.residual};
+        emit.slots = base + a.slot_off + w * (a.nslots * SLOT_BYTES);
+        emit.resbar = resbar + w * (MAX_SLOTS * 8);
+        emit.sm = reinterpret_cast<float*>(smem + a.slot_off + w * EXCHANGE_BYTES);
+        emit.sbias = reinterpret_cast<float*>(smem + a.sm_off + w * BIAS_BYTES);
+        emit.abort = s_abort;
+        emit.lane = lane;
+        auto place = [&](int u, int& row, int& col, int& k0, int& k1, int& sp) {
+            int im, in;
             unit_of(u, im, in, k0, k1, sp);
-            const int col0 = in * a.bn + h * half;
-            const Emit<T> emit{a, (T*)a.y + sp * a.part, (T*)a.z, (const T*)a.bias, (const T*)a.residual,
-                               (im * CG + rank) * BM + q * 32 + lane};
-            uint32_t res[Pack32<T>::N];
-            if constexpr (PB == 0) {
-                emit.ahead(res, col0);
-                const int buf = ci & 1;
-                ok = ptx::mbar_wait(accfull + buf * 8, (ci >> 1) & 1, s_abort, a.status, WAIT_LIMIT);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                for (int j = 0; j < half; j += 32) {
-                    float v[32];
-                    ptx::tmem_ld32(lanes + buf * 256 + j, v);
-                    if (j + 32 >= half) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cg<CG>(accempty + buf * 8);
-                    }
-                    emit(v, res, col0 + j);
-                    if (j + 32 < half) emit.ahead(res, col0 + j + 32);
+            row = (im * CG + rank) * BM + q * 32;
+            col = in * a.bn + h * half;
+        };
+        auto wait_acc = [&]() {
+            const bool ok = ptx::mbar_wait(accfull + buf * 8, phase, s_abort, a.status, WAIT_LIMIT);
+            const bool all = __all_sync(~0u, ok && emit.ok);
+            ptx::tc_fence_after();
+            return all;
+        };
+        auto free_acc = [&]() {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cg<CG>(accempty + buf * 8);
+            buf ^= 1;
+            phase ^= buf ^ 1;
+        };
+        // the residual's cursor: the next chunk to fetch, nslots - 1 ahead of the one written
+        const bool has_res = a.residual && a.tma_out;
+        int fu = group, fc = 0;
+        auto fetch_next = [&]() {
+            while (fu < units) {
+                int row, col, k0, k1, sp;
+                place(fu, row, col, k0, k1, sp);
+                col += fc * COLS;
+                const bool there = nch > 0 && emit.active(row, col);
+                if (++fc >= nch) fc = 0, fu += groups;
+                if (there) {
+                    emit.fetch(row, col);
+                    return;
                 }
-                ++ci;
+            }
+        };
+        if (has_res)
+            for (int i = 0; i < a.nslots - 1; ++i) fetch_next();
+        // the bias of a tile is loaded while the tile before is written
+        const bool has_bias = a.bias && a.tma_out;
+        float bnext[4] = {};
+        auto load_bias = [&](int u) {
+            int row, col, k0, k1, sp;
+            place(u, row, col, k0, k1, sp);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                bnext[i] = i * 32 < half && col + i * 32 + lane < a.cols ? ld1((const T*)a.bias + col + i * 32 + lane) : 0.f;
+        };
+        if (has_bias && group < units) load_bias(group);
+        for (int u = group; u < units; u += groups) {
+            int row, col, k0, k1, sp;
+            place(u, row, col, k0, k1, sp);
+            emit.row0 = row;
+            emit.sp = sp;
+            if (has_bias) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) emit.sbias[i * 32 + lane] = bnext[i];
+                __syncwarp();
+                if (u + groups < units) load_bias(u + groups);
+            }
+            auto write = [&](float(&v)[COLS], int c) {
+                const int before = emit.out;
+                emit.chunk(v, col + c * COLS, c * COLS, PB != 256 && (PB != 0 || std::is_same<T, bf16>::value));
+                if (has_res && emit.out != before) {
+                    emit.freed();
+                    fetch_next();
+                }
+            };
+            if constexpr (PB == 0) {
+                if (!wait_acc()) break;
+                const uint32_t acc = lanes + buf * 256;
+                if (nch == 0) free_acc();
+                for (int c = 0; c < nch; ++c) {
+                    float v[COLS];
+                    uint32_t r[COLS / 32][32];
+#pragma unroll
+                    for (int i = 0; i < COLS / 32; ++i) ptx::tmem_ld32_issue(acc + c * COLS + i * 32, r[i]);
+#pragma unroll
+                    for (int i = 0; i < COLS / 32; ++i) ptx::tmem_wait_ld(r[i]);
+                    if (c + 1 == nch) free_acc();
+#pragma unroll
+                    for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]);
+                    write(v, c);
+                }
             } else {
                 float acc[PB / 2] = {};
-                for (int c0 = k0; c0 < k1; c0 += a.chunk, ++ci) {
-                    const int buf = ci & 1;
-                    ok = ptx::mbar_wait(accfull + buf * 8, (ci >> 1) & 1, s_abort, a.status, WAIT_LIMIT);
-                    ok = __all_sync(~0u, ok);
+                bool ok = true;
+                for (int c0 = k0; c0 < k1; c0 += a.chunk) {
+                    ok = wait_acc();
                     if (!ok) break;
-                    ptx::tc_fence_after();
+                    const uint32_t from = lanes + buf * 256;
 #pragma unroll
                     for (int j = 0; j < PB / 2; j += 32) {
                         float v[32];
-                        ptx::tmem_ld32(lanes + buf * 256 + j, v);
+                        ptx::tmem_ld32(from + j, v);
                         if (PB <= 128 && a.ta > 1) {
-                            float w[32];
-                            ptx::tmem_ld32(lanes + buf * 256 + 128 + j, w);
+                            float l[32];
+                            ptx::tmem_ld32(from + 128 + j, l);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += w[i];
+                            for (int i = 0; i < 32; ++i) v[i] += l[i];
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[j + i] += v[i];
                     }
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cg<CG>(accempty + buf * 8);
+                    free_acc();
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < PB / 2; j += 32) {
-                    float(&v)[32] = *reinterpret_cast<float(*)[32]>(&acc[j]);
-                    if constexpr (PB == 256) {  // grad_weight, one term: no epilogue
-                        emit.plain(v, col0 + j);
-                    } else {
-                        emit.ahead(res, col0 + j);
-                        emit(v, res, col0 + j);
-                    }
-                }
+                for (int j = 0; j < PB / 2; j += 32) write(*reinterpret_cast<float(*)[32]>(&acc[j]), j / 32);
             }
         }
+        // residual chunks asked for have landed, and stores have read their slots, before the CTA leaves (bounded)
+        if (has_res)
+            for (int i = emit.out; i < emit.in; ++i) {
+                volatile int none = 0;
+                ptx::mbar_wait(emit.resbar + (i % a.nslots) * 8, (i / a.nslots) & 1, &none, a.status, WAIT_LIMIT);
+            }
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
     }
 
     ptx::tc_fence_before();
@@ -474,7 +602,7 @@ __global__ void __launch_bounds__(256) reduce_kernel(const float* __restrict__ p
                 if (bias) s += ld1(bias + n + c);
                 if (residual) s += ld1(residual + at);
                 if (z) z[at] = from_float<T>(s);
-                y[at] = from_float<T>(act_run(s, act));
+                y[at] = from_float<T>(act_run<kFast<T>>(s, act));
             }
     }
 }
@@ -613,7 +741,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const
                 float s[8];
                 load8<VEC>(s, saved + at, N - c);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = act_grad<ACT>(v[q], s[q]);
+                for (int q = 0; q < 8; ++q) v[q] = act_grad<ACT, kFast<T>>(v[q], s[q]);
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q) sum[q] += v[q];
@@ -676,7 +804,7 @@ struct Matrix {
 
 // Its tensor map with boxes of 64 columns and `box` rows.
 bool encode(CUtensorMap* m, const Matrix& x, int box) {
-    auto fn = encode_fn();
+    const auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)x.terms};
     cuuint64_t strides[2] = {(cuuint64_t)x.pitch * 2, (cuuint64_t)x.pitch * 2 * x.rows};
@@ -684,6 +812,20 @@ bool encode(CUtensorMap* m, const Matrix& x, int box) {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The map of a result's chunks (128 bytes of 32 rows): [parts][rows][pitch] of T.
+template <typename T>
+bool encode_out(CUtensorMap* m, const void* p, int rows, int cols, int pitch, int parts) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    constexpr bool f32 = std::is_same<T, float>::value;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch * sizeof(T), (cuuint64_t)pitch * sizeof(T) * rows};
+    cuuint32_t b[3] = {128 / sizeof(T), 32, 1}, es[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims,
+              strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename... P, typename... Q>
@@ -727,6 +869,7 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
             for (int bn = 64; bn <= (prods > 1 ? 128 : 256); bn *= 2) {
                 if (cg == 2 && bn < 128) continue;
                 if (bn > 64 && bn / 2 >= c) continue;
+                if (prods == 6 && cg == 1 && bn == 128) continue;  // shared memory holds one stage only
                 const long long mt = (r + BM * cg - 1) / (BM * cg), nt = (c + bn - 1) / bn;
                 const int slots = sms / cg;
                 const double stage = std::max(2.0 * bn * prods, (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
@@ -757,12 +900,11 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
 }
 
 template <typename T, int PB, int CG>
-cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int grid, uint32_t smem,
-                        cudaStream_t st) {
+cudaError_t launch_gemm(const CUtensorMap (&m)[5], const GemmArgs& a, int grid, uint32_t smem, cudaStream_t st) {
     static DeviceFlags attr;
     cudaError_t e = max_dynamic_smem_once((const void*)gemm_tc_kernel<T, PB, CG>, SMEM_MAX, attr);
     if (e != cudaSuccess) return e;
-    return launch(gemm_tc_kernel<T, PB, CG>, grid, THREADS, smem, CG, st, ma, mb, a);
+    return launch(gemm_tc_kernel<T, PB, CG>, grid, THREADS, smem, CG, st, m[0], m[1], m[2], m[3], m[4], a);
 }
 
 template <typename T>
@@ -798,8 +940,6 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.a_mn = l_mn;
     a.b_mn = r_mn;
     a.stage_bytes = L.terms * A_BYTES + R.terms * (uint32_t)(p.bn / p.cg) * 128;
-    a.stages = (int)std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 1024 - BAR_BYTES) / a.stage_bytes);
-    a.bar_off = a.stages * a.stage_bytes;
     a.status = status;
     const bool split = p.splits > 1;
     const int pitch = split ? (cols + 7) / 8 * 8 : cols;
@@ -808,7 +948,7 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.part = (long long)rows * pitch;
     if (split) {
         a.y = parts;
-        a.vec = p.swap ? 0 : 2;
+        a.tma_out = !p.swap;
     } else {
         a.bias = out.bias;
         a.residual = out.residual;
@@ -816,19 +956,39 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
         a.z = out.z;
         a.act = out.act;
         const uintptr_t all = (uintptr_t)out.y | (uintptr_t)out.z | (uintptr_t)out.residual | (uintptr_t)(pitch * sizeof(T));
-        a.vec = p.swap ? 0 : all % 32 == 0 ? 2 : all % 16 == 0 ? 1 : 0;
+        a.tma_out = !p.swap && all % 16 == 0;
     }
-    CUtensorMap ma, mb;
-    if (!encode(&ma, L, l_mn ? BK : BM) || !encode(&mb, R, r_mn ? BK : p.bn / p.cg)) return cudaErrorInvalidValue;
+    // Two slots a warp, so that one is written while the other is stored; a third lets the residual run two chunks
+    // ahead. Long reductions, whose epilogue is rare, leave the room to the operands' stages.
+    if (a.residual)
+        a.nslots = a.kblocks <= 8 && L.terms == 1 ? 3 : 2;
+    else
+        a.nslots = a.kblocks <= 16 && L.terms == 1 ? 2 : 1;
+    const uint32_t epi = EPI_WARPS * (a.tma_out ? a.nslots * SLOT_BYTES : EXCHANGE_BYTES);
+    const uint32_t extra = epi + BAR_BYTES + EPI_WARPS * BIAS_BYTES;
+    a.stages = (int)std::min<uint32_t>(MAX_STAGES, (SMEM_MAX - 1024 - extra) / a.stage_bytes);
+    a.slot_off = a.stages * a.stage_bytes;
+    a.bar_off = a.slot_off + epi;
+    a.sm_off = a.bar_off + BAR_BYTES;
+    if (a.stages < 1) return cudaErrorInvalidConfiguration;
+    CUtensorMap m[5] = {};
+    if (!encode(&m[0], L, l_mn ? BK : BM) || !encode(&m[1], R, r_mn ? BK : p.bn / p.cg)) return cudaErrorInvalidValue;
+    if (a.tma_out) {
+        bool good = split ? encode_out<float>(&m[2], parts, rows, cols, pitch, p.splits)
+                          : encode_out<T>(&m[2], out.y, rows, cols, pitch, 1);
+        if (a.z) good = good && encode_out<T>(&m[3], out.z, rows, cols, pitch, 1);
+        if (a.residual) good = good && encode_out<T>(&m[4], out.residual, rows, cols, pitch, 1);
+        if (!good) return cudaErrorInvalidValue;
+    }
     const long long units = (long long)a.mt * a.nt * a.splits;
     const int grid = (int)std::min<long long>(units, num_sms() / p.cg) * p.cg;
-    const uint32_t smem = a.bar_off + BAR_BYTES + 1024;
+    const uint32_t smem = a.slot_off + extra + 1024;
     cudaError_t e;
     auto go = [&](auto t, auto pb) {
         using D = decltype(t);
         constexpr int PB = decltype(pb)::value;
-        return p.cg == 2 ? launch_gemm<D, PB, 2>(ma, mb, a, grid, smem, st)
-                         : launch_gemm<D, PB, 1>(ma, mb, a, grid, smem, st);
+        return p.cg == 2 ? launch_gemm<D, PB, 2>(m, a, grid, smem, st)
+                         : launch_gemm<D, PB, 1>(m, a, grid, smem, st);
     };
     if (f32_out) {
         e = p.bn == 64    ? go(float{}, std::integral_constant<int, 64>{})
