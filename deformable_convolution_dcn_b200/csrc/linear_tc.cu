@@ -16,8 +16,8 @@
 // rather than rounding it, so float32 results take the accumulator out every
 // `chunk` blocks of 64 and add it in registers with proper rounding.
 //
-// Warps: 0 TMA producer, 1 MMA issue and TMEM, 2-9 epilogue (each of the four
-// TMEM lane quarters twice, once for each half of the columns). Accumulators
+// Warps: 0 and 10 TMA producers of A and B, 1 MMA issue and TMEM, 2-9 epilogue
+// (each of the four TMEM lane quarters twice, once for each half of the columns). Accumulators
 // are double buffered: the epilogue of a tile overlaps the next one's MMAs. The
 // epilogue adds bias and residual, applies the activation and stores whole
 // 32-byte sectors. Products with too few tiles to fill the GPU are split along
@@ -37,7 +37,8 @@ namespace {
 
 constexpr int BM = 128, BK = 64;          // lanes a CTA, reduction elements a stage
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + EPI_WARPS * 32;
+constexpr int B_WARP = 2 + EPI_WARPS;     // the second producer
+constexpr int THREADS = (B_WARP + 1) * 32;
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t A_BYTES = BM * BK * 2; // one term of one stage
 constexpr uint32_t MN_BLOCK = BK * 128;   // 64 rows of an MN-major operand over a stage: 8 KB
@@ -47,14 +48,20 @@ constexpr uint32_t SLOT_BYTES = 4096, EXCHANGE_BYTES = 32 * 33 * 4, BIAS_BYTES =
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long WAIT_LIMIT = 2000000000LL;
 
+// How the TMA producer walks an operand (see encode()).
+constexpr int kKMajor = 0, kMnBlocks = 1, kMnRows = 2;
+struct Operand {
+    int terms;  // bfloat16 terms: 1 or 3
+    int kind;
+};
+
 struct GemmArgs {
     int rows, cols;        // D: A-side rows, B-side rows
     int kblocks, splits;   // stages of 64; parts along the reduction
     int chunk;             // stages between two reads of the accumulator
     int mt, nt;            // tiles
     int bn;                // B rows a tile (of the CTA or pair)
-    int ta, tb;            // bfloat16 terms of A, B
-    int a_mn, b_mn;        // operand is MN-major
+    Operand a, b;
     int stages;
     uint32_t stage_bytes, bar_off;
     // epilogue: D[i, j] goes to element i * rs + j * cs
@@ -157,7 +164,7 @@ struct Emit {
         if (lane == 0) {
             const int s = in % a.nslots;
             ptx::mbar_arrive_expect_tx(resbar + s * 8, 4096);
-            ptx::tma_load_3d<1>(slots + s * 4096, mr, resbar + s * 8, col, row, 0);
+            ptx::tma_load_3d(slots + s * 4096, mr, resbar + s * 8, col, row, 0);
         }
         ++in;
     }
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) {
         for (int i = 0; i < MAX_STAGES; ++i) {
-            ptx::mbar_init(full + i * 8, 1);
+            ptx::mbar_init(full + i * 8, 2);  // both producers
             ptx::mbar_init(empty + i * 8, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -320,59 +327,69 @@ __global__ void __launch_bounds__(THREADS, 1)
         k1 = (int)((long long)a.kblocks * (sp + 1) / a.splits);
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // ---- TMA producer: this CTA's rows of A, its share of B's rows
-            const int bn = a.bn / CG;
-            int stage = 0, it = 0;
-            uint32_t phase = 1;  // of the empty barrier: the first round of stages is free
-            bool ok = true;
-            for (int u = group; u < units && ok; u += groups) {
-                int im, in, k0, k1, sp;
-                unit_of(u, im, in, k0, k1, sp);
-                const int r0 = (im * CG + rank) * BM, c0 = in * a.bn + rank * bn;
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    ok = ptx::mbar_wait(empty + stage * 8, phase, s_abort, a.status, WAIT_LIMIT);
-                    if (!ok) break;
-                    const uint32_t bar = full + stage * 8;
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, a.stage_bytes * CG);
-                    uint32_t dst = base + stage * a.stage_bytes;
-                    for (int t = 0; t < a.ta; ++t, dst += A_BYTES) {
-                        if (a.a_mn) {
-                            ptx::tma_load_3d<CG>(dst, &tma, bar, r0, kb * BK, t);
-                            ptx::tma_load_3d<CG>(dst + MN_BLOCK, &tma, bar, r0 + 64, kb * BK, t);
-                        } else {
-                            ptx::tma_load_3d<CG>(dst, &tma, bar, kb * BK, r0, t);
+    if (warp == 0 || warp == B_WARP) {
+        // ---- TMA producers, one for each operand: this CTA's rows of A, its share of B's rows. The whole warp walks
+        // the loop and one elected lane issues. (One warp for both took 640 cycles a stage, whatever its size: the
+        // issue of a load costs about 200, and a stage's MMAs take 2 bn.)
+        const bool isb = warp == B_WARP;
+        const Operand& o = isb ? a.b : a.a;
+        const CUtensorMap* map = isb ? &tmb : &tma;
+        const int rows = isb ? a.bn / CG : BM;
+        const uint32_t term_bytes = (uint32_t)rows * 128, bytes = term_bytes * o.terms;
+        const uint32_t first = base + (isb ? a.a.terms * A_BYTES : 0);
+        int stage = 0, it = 0;
+        uint32_t phase = 1;  // of the empty barrier: the first round of stages is free
+        bool ok = true;
+        for (int u = group; u < units && ok; u += groups) {
+            int im, in, k0, k1, sp;
+            unit_of(u, im, in, k0, k1, sp);
+            const int r0 = isb ? in * a.bn + rank * rows : (im * CG + rank) * BM;
+            // coordinates: K-major (64 kb, row, 0), MN-major in one box (0, 64 kb, row / 64) or a box for each 64 rows
+            // (row, 64 kb, 0)
+            const int x0 = o.kind == kMnRows ? r0 : 0, dx = o.kind == kKMajor ? BK : 0;
+            const int y0 = o.kind == kKMajor ? r0 : 0, dy = BK - dx, z0 = o.kind == kMnBlocks ? r0 / 64 : 0;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                ok = ptx::mbar_wait(empty + stage * 8, phase, s_abort, a.status, WAIT_LIMIT);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                if (ptx::elect_one()) {
+                    const uint32_t bar = full + stage * 8, dst = first + stage * a.stage_bytes;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes * CG);
+                    const int x = x0 + kb * dx, y = y0 + kb * dy;
+                    if (o.kind != kMnRows) {
+                        ptx::tma_load_4d_cg<CG>(dst, map, bar, x, y, z0, 0);
+                        if (o.terms > 1) {
+                            ptx::tma_load_4d_cg<CG>(dst + term_bytes, map, bar, x, y, z0, 1);
+                            ptx::tma_load_4d_cg<CG>(dst + 2 * term_bytes, map, bar, x, y, z0, 2);
                         }
+                    } else {
+                        for (int t = 0; t < o.terms; ++t)
+                            for (int h = 0; h < rows / 64; ++h)
+                                ptx::tma_load_4d_cg<CG>(dst + t * term_bytes + h * MN_BLOCK, map, bar, x + h * 64, y, 0,
+                                                        t);
                     }
-                    for (int t = 0; t < a.tb; ++t, dst += bn * 128) {
-                        if (a.b_mn) {
-                            for (int h = 0; h < bn / 64; ++h)
-                                ptx::tma_load_3d<CG>(dst + h * MN_BLOCK, &tmb, bar, c0 + h * 64, kb * BK, t);
-                        } else {
-                            ptx::tma_load_3d<CG>(dst, &tmb, bar, kb * BK, c0, t);
-                        }
-                    }
-                    if (++stage == a.stages) stage = 0, phase ^= 1;
                 }
-            }
-            // copies still in flight land before the CTA may exit (bounded)
-            if (rank == 0) {
-                volatile int none = 0;
-                for (int k = std::max(0, it - a.stages); k < it; ++k)
-                    ptx::mbar_wait(full + (k % a.stages) * 8, (k / a.stages) & 1, &none, nullptr, WAIT_LIMIT);
+                __syncwarp();
+                if (++stage == a.stages) stage = 0, phase ^= 1;
             }
         }
+        // copies still in flight land before the CTA may exit (bounded)
+        if (rank == 0 && lane == 0) {
+            volatile int none = 0;
+            for (int k = std::max(0, it - a.stages); k < it; ++k)
+                ptx::mbar_wait(full + (k % a.stages) * 8, (k / a.stages) & 1, &none, nullptr, WAIT_LIMIT);
+        }
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---- MMA issue. The loop is one thread's serial work: it keeps nothing that needs a division or a
-            // 64-bit sum per step (with both, a stage took 850 cycles whatever its size; its MMAs take 2 bn)
+        if (rank == 0) {
+            // ---- MMA issue, by one elected lane. The loop keeps nothing that needs a division or a 64-bit sum per step
+            const bool a_mn = a.a.kind != kKMajor, b_mn = a.b.kind != kKMajor;
             const uint32_t idesc =
-                ptx::idesc_bf16_f32(BM * CG, a.bn) | ((uint32_t)a.a_mn << 15) | ((uint32_t)a.b_mn << 16);
-            const OperandDesc da(base, a.a_mn), db(base + a.ta * A_BYTES, a.b_mn);
+                ptx::idesc_bf16_f32(BM * CG, a.bn) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+            const OperandDesc da(base, a_mn), db(base + a.a.terms * A_BYTES, b_mn);
             const uint32_t aterm = A_BYTES / 16, bterm = (uint32_t)(a.bn / CG) * 128 / 16;
             const uint32_t stage_units = a.stage_bytes / 16;
-            const bool many = a.ta > 1, both = a.tb > 1;
+            const bool many = a.a.terms > 1, both = a.b.terms > 1;
             int stage = 0;
             uint32_t phase = 0, acc_phase = 1, off = 0;
             int buf = 0;
@@ -382,50 +399,54 @@ __global__ void __launch_bounds__(THREADS, 1)
                 unit_of(u, im, in, k0, k1, sp);
                 for (int c0 = k0; c0 < k1 && ok; c0 += a.chunk) {
                     ok = ptx::mbar_wait(accempty + buf * 8, acc_phase, s_abort, a.status, WAIT_LIMIT);
+                    ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t acc = tmem + buf * 256, low = acc + 128;
                     const int c1 = min(c0 + a.chunk, k1);
-                    uint32_t more = 0;
                     for (int kb = c0; kb < c1; ++kb) {
                         ok = ptx::mbar_wait(full + stage * 8, phase, s_abort, a.status, WAIT_LIMIT);
+                        ok = __all_sync(~0u, ok);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        if (!many) {
+                        if (ptx::elect_one()) {
+                            const uint32_t first = kb > c0;
+                            if (!many) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                ptx::mma_bf16_cg<CG>(acc, da.at(off, k), db.at(off, k), idesc, more);
-                                more = 1;
-                            }
-                        } else {
+                                for (int k = 0; k < 4; ++k)
+                                    ptx::mma_bf16_cg<CG>(acc, da.at(off, k), db.at(off, k), idesc, k ? 1u : first);
+                            } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint64_t a0 = da.at(off, k), b0 = db.at(off, k);
-                                ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
-                                ptx::mma_bf16_cg<CG>(low, da.at(off + 2 * aterm, k), b0, idesc, more);
-                                more = 1;
-                                const uint64_t a1 = da.at(off + aterm, k);
-                                ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, 1u);
-                                if (both) {
-                                    const uint64_t b1 = db.at(off + bterm, k);
-                                    ptx::mma_bf16_cg<CG>(low, a0, db.at(off + 2 * bterm, k), idesc, 1u);
-                                    ptx::mma_bf16_cg<CG>(low, a1, b1, idesc, 1u);
-                                    ptx::mma_bf16_cg<CG>(low, a0, b1, idesc, 1u);
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t more = k ? 1u : first;
+                                    const uint64_t a0 = da.at(off, k), b0 = db.at(off, k);
+                                    ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
+                                    ptx::mma_bf16_cg<CG>(low, da.at(off + 2 * aterm, k), b0, idesc, more);
+                                    const uint64_t a1 = da.at(off + aterm, k);
+                                    ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, 1u);
+                                    if (both) {
+                                        const uint64_t b1 = db.at(off + bterm, k);
+                                        ptx::mma_bf16_cg<CG>(low, a0, db.at(off + 2 * bterm, k), idesc, 1u);
+                                        ptx::mma_bf16_cg<CG>(low, a1, b1, idesc, 1u);
+                                        ptx::mma_bf16_cg<CG>(low, a0, b1, idesc, 1u);
+                                    }
                                 }
                             }
+                            ptx::mma_commit_cg<CG>(empty + stage * 8);
+                            if (kb + 1 == c1) ptx::mma_commit_cg<CG>(accfull + buf * 8);
                         }
-                        ptx::mma_commit_cg<CG>(empty + stage * 8);
+                        __syncwarp();
                         off += stage_units;
                         if (++stage == a.stages) stage = 0, off = 0, phase ^= 1;
                     }
-                    ptx::mma_commit_cg<CG>(accfull + buf * 8);
                     buf ^= 1;
                     acc_phase ^= buf ^ 1;
                 }
             }
             // every issued MMA has completed before TMEM and shared memory are released (bounded)
             volatile int none = 0;
-            ptx::mma_commit_cg<CG>(done);
+            if (ptx::elect_one()) ptx::mma_commit_cg<CG>(done);
+            __syncwarp();
             ptx::mbar_wait(done, 0, &none, a.status, WAIT_LIMIT);
         }
     } else {
@@ -538,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int j = 0; j < PB / 2; j += 32) {
                         float v[32];
                         ptx::tmem_ld32(from + j, v);
-                        if (PB <= 128 && a.ta > 1) {
+                        if (PB <= 128 && a.a.terms > 1) {
                             float l[32];
                             ptx::tmem_ld32(from + 128 + j, l);
 #pragma unroll
@@ -802,14 +823,20 @@ struct Matrix {
     int rows, cols, pitch, terms;
 };
 
-// Its tensor map with boxes of 64 columns and `box` rows.
-bool encode(CUtensorMap* m, const Matrix& x, int box) {
+// Its tensor map for `rows` operand rows a stage. K-major: boxes of 64 reduction elements and `rows` rows. MN-major:
+// 64 reduction rows and 64 operand rows (128 bytes) a block; where the blocks tile the matrix exactly, they are a
+// dimension of their own and one box holds all of a stage's.
+bool encode(CUtensorMap* m, const Matrix& x, bool mn, int rows, int* kind) {
     const auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)x.terms};
-    cuuint64_t strides[2] = {(cuuint64_t)x.pitch * 2, (cuuint64_t)x.pitch * 2 * x.rows};
-    cuuint32_t b[3] = {64, (cuuint32_t)box, 1}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, b, es,
+    const bool blocks = mn && x.cols % 64 == 0;
+    *kind = !mn ? kKMajor : blocks ? kMnBlocks : kMnRows;
+    cuuint64_t dims[4] = {(cuuint64_t)(blocks ? 64 : x.cols), (cuuint64_t)x.rows, (cuuint64_t)(blocks ? x.cols / 64 : 1),
+                          (cuuint64_t)x.terms};
+    const cuuint64_t plane = (cuuint64_t)x.pitch * 2 * x.rows;
+    cuuint64_t strides[3] = {(cuuint64_t)x.pitch * 2, blocks ? 128 : plane, plane};
+    cuuint32_t b[4] = {64, (cuuint32_t)(mn ? BK : rows), (cuuint32_t)(blocks ? rows / 64 : 1), 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.p), dims, strides, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -935,10 +962,8 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.mt = (a.rows + BM * p.cg - 1) / (BM * p.cg);
     a.nt = (a.cols + p.bn - 1) / p.bn;
     a.bn = p.bn;
-    a.ta = L.terms;
-    a.tb = R.terms;
-    a.a_mn = l_mn;
-    a.b_mn = r_mn;
+    a.a.terms = L.terms;
+    a.b.terms = R.terms;
     a.stage_bytes = L.terms * A_BYTES + R.terms * (uint32_t)(p.bn / p.cg) * 128;
     a.status = status;
     const bool split = p.splits > 1;
@@ -972,7 +997,8 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.sm_off = a.bar_off + BAR_BYTES;
     if (a.stages < 1) return cudaErrorInvalidConfiguration;
     CUtensorMap m[5] = {};
-    if (!encode(&m[0], L, l_mn ? BK : BM) || !encode(&m[1], R, r_mn ? BK : p.bn / p.cg)) return cudaErrorInvalidValue;
+    if (!encode(&m[0], L, l_mn, BM, &a.a.kind) || !encode(&m[1], R, r_mn, p.bn / p.cg, &a.b.kind))
+        return cudaErrorInvalidValue;
     if (a.tma_out) {
         bool good = split ? encode_out<float>(&m[2], parts, rows, cols, pitch, p.splits)
                           : encode_out<T>(&m[2], out.y, rows, cols, pitch, 1);

@@ -313,22 +313,28 @@ __device__ __forceinline__ float to_tf32(float x) {
 // ------------------------------------------------- pairs of CTAs (cta_group::2) --
 // CG = 1: one CTA; CG = 2: the two CTAs of a cluster, whose MMAs the even one issues.
 
-// 3-D tiled bulk tensor load into this CTA's shared memory; with CG = 2 the
+// 4-D tiled bulk tensor load into this CTA's shared memory; with CG = 2 the
 // bytes are counted on the even CTA's barrier at the same offset. (No multicast.)
 template <int CG>
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+__device__ __forceinline__ void tma_load_4d_cg(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                               int c2, int c3) {
     if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-            "[%2];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-            : "memory");
+        tma_load_4d(dst, map, bar, c0, c1, c2, c3);
     else
         asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar & 0xFEFFFFFFu), "r"(x), "r"(y), "r"(z)
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+            "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar & 0xFEFFFFFFu), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
             : "memory");
+}
+
+// 3-D tiled bulk tensor load into this CTA's shared memory. (No multicast.)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
 template <int CG>
@@ -389,6 +395,19 @@ __device__ __forceinline__ void mbar_arrive_cg(uint32_t bar) {
             "mapa.shared::cluster.u32 r, %0, 0;\n\t"
             "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
             : "memory");
+}
+
+// True in one lane of a converged warp. Under it the compiler knows that a single
+// lane runs and that the other operands are uniform, which a test of the lane
+// number does not tell it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
