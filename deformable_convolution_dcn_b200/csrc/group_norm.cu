@@ -20,6 +20,7 @@
 
 #include "act.cuh"
 #include "kernels.h"
+#include "norm.cuh"
 
 namespace dcn {
 namespace {
@@ -102,33 +103,17 @@ __device__ __forceinline__ Cols cols_of(const NormShape& s, const Plan& p, int b
 
 template <typename T, int V>
 __device__ __forceinline__ void load(float (&v)[V], const T* p) {
-    if constexpr (V == 1) {
+    if constexpr (V == 1)
         v[0] = ld1(p);
-    } else if constexpr (V == 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p));
-        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
+    else
+        unpack(v, __ldg(reinterpret_cast<const uint4*>(p)));
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
-    if constexpr (V == 1) {
+    if constexpr (V == 1)
         *p = from_float<T>(v[0]);
-    } else if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-        __nv_bfloat162 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(h);
-    }
+    else
+        *reinterpret_cast<uint4*>(p) = pack<T>(v);
 }
 
 // Joins (n, mean, m2) of two disjoint sets of values.
@@ -258,24 +243,6 @@ __global__ void __launch_bounds__(NT) apply_kernel(const NormShape s, const Plan
         for (int i = 0; i < V; ++i) v[i] = act_apply<ACT, kFast<T>>(fmaf(v[i] - mean[i], a[i], be[i]));
         store<T, V>(y + at + (size_t)r * s.C, v);
     }
-}
-
-// relu's slope where z is too near its border for float32 to say the sign: the sign of z in float64
-__device__ __noinline__ bool positive64(float x, float mean, float rstd, float ga, float be) {
-    return ((double)x - (double)mean) * (double)rstd * (double)ga + (double)be > 0.0;
-}
-
-// dz of one value. hat = (x - mean) rstd.
-template <int ACT, bool FAST>
-__device__ __forceinline__ float dz_of(float gy, float x, float hat, float mean, float rstd, float ga, float be) {
-    const float z = fmaf(hat, ga, be);
-    if constexpr (ACT == kActRelu) {
-        bool up = z > 0.f;
-        if (fabsf(z) < 1e-5f * (fabsf(hat * ga) + fabsf(be)))
-            up = positive64(x, mean, rstd, ga, be);
-        return up ? gy : 0.f;
-    }
-    return act_grad<ACT, FAST>(gy, z);
 }
 
 // sums[(b * chunks + chunk) * C + c] = (sum dz, sum dz xh) over the chunk's pixels
@@ -495,7 +462,7 @@ cudaError_t backward_t(const NormShape& s, bool vec, const void* x, const void* 
 }  // namespace
 
 size_t norm_workspace(const NormShape& s, int bf, bool backward) {
-    size_t most = 0;
+    size_t most = backward ? (size_t)s.B * s.C * sizeof(float2) : 0;  // by clusters
     for (int v : {bf ? 8 : 4, s.C + 1}) {  // vectors, or (an unaligned map) single values
         const Plan p = make_plan(s, v);
         const size_t n = (size_t)s.B * p.chunks;
@@ -507,6 +474,10 @@ size_t norm_workspace(const NormShape& s, int bf, bool backward) {
 
 cudaError_t norm_forward(const NormShape& s, int bf, bool vec, const void* x, const void* gamma, const void* beta,
                          void* y, float* stats, void* ws, cudaStream_t st, int* launches) {
+    if (vec && norm_cluster_supported(s, bf, false)) {
+        ++*launches;
+        return norm_cluster_forward(s, bf, x, gamma, beta, y, stats, st);
+    }
     return bf ? forward_t<bf16>(s, vec, x, gamma, beta, y, stats, ws, st, launches)
               : forward_t<float>(s, vec, x, gamma, beta, y, stats, ws, st, launches);
 }
@@ -514,6 +485,18 @@ cudaError_t norm_forward(const NormShape& s, int bf, bool vec, const void* x, co
 cudaError_t norm_backward(const NormShape& s, int bf, bool vec, const void* x, const void* gamma, const void* beta,
                           const float* stats, const void* gy, void* gx, float* gg, float* gb, void* ws,
                           cudaStream_t st, int* launches) {
+    if (vec && norm_cluster_supported(s, bf, true)) {
+        float2* sums = gg || gb ? (float2*)ws : nullptr;
+        cudaError_t e = norm_cluster_backward(s, bf, x, gamma, beta, stats, gy, sums, gx, st);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        if (sums) {
+            bwd_params_kernel<<<(s.C + 31) / 32, NT, 0, st>>>(s, s.B, (const float2*)ws, gg, gb);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            ++*launches;
+        }
+        return e;
+    }
     return bf ? backward_t<bf16>(s, vec, x, gamma, beta, stats, gy, gx, gg, gb, ws, st, launches)
               : backward_t<float>(s, vec, x, gamma, beta, stats, gy, gx, gg, gb, ws, st, launches);
 }

@@ -149,6 +149,15 @@ cudaError_t norm_backward(const NormShape& s, int dtype_bf16, bool vec, const vo
                           const void* beta, const float* stats, const void* gy, void* gx, float* gg, float* gb,
                           void* ws, cudaStream_t st, int* launches);
 
+// group_norm_cluster.cu — the same in one pass over HBM, by clusters that keep a sample's block of channels in shared
+// memory; maps whose blocks fit (x, y, grad_y, grad_x 16-byte aligned). sums [B][C]: (sum dz, sum dz xh), may be null.
+bool norm_cluster_supported(const NormShape& s, int dtype_bf16, bool backward);
+cudaError_t norm_cluster_forward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma,
+                                 const void* beta, void* y, float* stats, cudaStream_t st);
+cudaError_t norm_cluster_backward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma,
+                                  const void* beta, const float* stats, const void* gy, float2* sums, void* gx,
+                                  cudaStream_t st);
+
 // selftest.cu — a kernel whose bounded wait can only give up (failure-detection test).
 cudaError_t selftest_wait_timeout(long long limit_cycles, cudaStream_t st);
 

@@ -518,6 +518,15 @@ __device__ __forceinline__ void ldg_v8(uint32_t (&v)[8], const void* p) {
         : "l"(p));
 }
 
+// 16 bytes read once: not kept in L1. Volatile so that a batch of these is in flight before the first is consumed.
+__device__ __forceinline__ uint4 ldg_v4_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ uint2 ldg_v2(const void* p) {
     uint2 v;
     asm("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
