@@ -726,9 +726,12 @@ int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const
     TRY(check_ptr(y, "y", es, true));
     TRY(check_ptr(stats, "stats", 4, false));
     TRY(norm_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+    unsigned* status = nullptr;
+    cudaError_t e = dcn::status_word_ptr(&status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word");
     int n = 0;
-    cudaError_t e = dcn::norm_forward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(y), x, gamma, beta, y,
-                                      stats, workspace, (cudaStream_t)stream, &n);
+    e = dcn::norm_forward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(y), x, gamma, beta, y, stats,
+                          workspace, status, (cudaStream_t)stream, &n);
     g_launches += n;
     if (e != cudaSuccess) return cuda_fail(e, "group norm forward launch");
     return ok();
@@ -751,10 +754,13 @@ int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, cons
     TRY(check_ptr(grad_beta, "grad_beta", 4, false));
     if (!grad_x && !grad_gamma && !grad_beta) return ok();
     TRY(norm_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+    unsigned* status = nullptr;
+    cudaError_t e = dcn::status_word_ptr(&status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word");
     int n = 0;
-    cudaError_t e = dcn::norm_backward(s, params->dtype == DCN_BF16,
-                                       aligned16(x) && aligned16(grad_y) && aligned16(grad_x), x, gamma, beta, stats,
-                                       grad_y, grad_x, grad_gamma, grad_beta, workspace, (cudaStream_t)stream, &n);
+    e = dcn::norm_backward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(grad_y) && aligned16(grad_x), x,
+                           gamma, beta, stats, grad_y, grad_x, grad_gamma, grad_beta, workspace, status,
+                           (cudaStream_t)stream, &n);
     g_launches += n;
     if (e != cudaSuccess) return cuda_fail(e, "group norm backward launch");
     return ok();

@@ -144,10 +144,11 @@ struct NormShape {
 };
 size_t norm_workspace(const NormShape& s, int dtype_bf16, bool backward);
 cudaError_t norm_forward(const NormShape& s, int dtype_bf16, bool vec, const void* x, const void* gamma,
-                         const void* beta, void* y, float* stats, void* ws, cudaStream_t st, int* launches);
+                         const void* beta, void* y, float* stats, void* ws, unsigned* status, cudaStream_t st,
+                         int* launches);
 cudaError_t norm_backward(const NormShape& s, int dtype_bf16, bool vec, const void* x, const void* gamma,
                           const void* beta, const float* stats, const void* gy, void* gx, float* gg, float* gb,
-                          void* ws, cudaStream_t st, int* launches);
+                          void* ws, unsigned* status, cudaStream_t st, int* launches);
 
 // group_norm_cluster.cu — the same in one pass over HBM, by clusters that keep a sample's block of channels in shared
 // memory; maps whose blocks fit (x, y, grad_y, grad_x 16-byte aligned). sums [B][C]: (sum dz, sum dz xh), may be null.
@@ -157,6 +158,16 @@ cudaError_t norm_cluster_forward(const NormShape& s, int dtype_bf16, const void*
 cudaError_t norm_cluster_backward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma,
                                   const void* beta, const float* stats, const void* gy, float2* sums, void* gx,
                                   cudaStream_t st);
+
+// group_norm_stream.cu — long maps of whole vectors: summed and applied from a queue, loads by a producer warp
+// (x, y, grad_y, grad_x 16-byte aligned).
+bool norm_stream_supported(const NormShape& s, int dtype_bf16, bool backward);
+size_t norm_stream_workspace(const NormShape& s, int dtype_bf16, bool backward);
+cudaError_t norm_stream_forward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma, const void* beta,
+                                void* y, float* stats, void* ws, unsigned* status, cudaStream_t st);
+cudaError_t norm_stream_backward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma,
+                                 const void* beta, const float* stats, const void* gy, void* gx, float* gg, float* gb,
+                                 void* ws, unsigned* status, cudaStream_t st);
 
 // selftest.cu — a kernel whose bounded wait can only give up (failure-detection test).
 cudaError_t selftest_wait_timeout(long long limit_cycles, cudaStream_t st);

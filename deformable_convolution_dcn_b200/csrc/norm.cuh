@@ -2,6 +2,7 @@
 #pragma once
 
 #include "act.cuh"
+#include "kernels.h"
 
 namespace dcn {
 
@@ -44,6 +45,19 @@ __device__ __forceinline__ float dz_of(float gy, float x, float hat, float mean,
         return up ? gy : 0.f;
     }
     return act_grad<ACT, FAST>(gy, z);
+}
+
+// grad_beta, grad_gamma: a channel's sums over the samples (sums [B][C])
+__device__ __forceinline__ void params_of(const NormShape& s, const float2* sums, int c, float* gg, float* gb) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int b = 0; b < s.B; ++b) {
+        const float2 q = __ldcg(sums + (size_t)b * s.C + c);
+        v.x += q.x;
+        v.y += q.y;
+    }
+    if (gb) gb[c] = v.x;
+    if (gg) gg[c] = v.y;
 }
 
 }  // namespace dcn
