@@ -4,7 +4,7 @@
 //
 // One block an SM. A producer warp claims the units and copies their pixels, which
 // lie in one run, to a ring of shared-memory stages (bulk copies, up to 150 KB in
-// flight); sixteen warps compute from there and store. So the memory works on while
+// flight); the other warps compute from there and store. So the memory works on while
 // a unit's sums are reduced, joined and released, and those latencies, which bound
 // the kernels without the ring (8x200x200x128: 92 us), cost nothing. The producer
 // also waits for a set's statistics before it copies a unit of the second pass, and
@@ -24,14 +24,13 @@
 namespace dcn {
 namespace {
 
-constexpr int NC = 512;                  // computing threads
-constexpr int WARPS = NC / 32;
-constexpr int THREADS = NC + 32;         // and the producer warp
+// computing threads (and a producer warp): the backward keeps twice the parameters in registers
+constexpr int NC_FWD = 768, NC_BWD = 512;
 constexpr int MAX_STAGES = 16;
 constexpr int MAX_C = 1024;
 constexpr int MAX_GROUPS = 256;          // their statistics travel in a stage
-constexpr uint32_t RING = 176 * 1024;    // all stages
-constexpr uint32_t RED_BYTES = 2 * NC * 8 * 4;
+constexpr uint32_t RING = 168 * 1024;    // all stages
+constexpr uint32_t RED_BYTES = 2 * NC_FWD * 8 * 4;
 constexpr long long WAIT_LIMIT = 2000000000LL;
 
 struct StreamPlan {
@@ -46,9 +45,9 @@ StreamPlan stream_plan(const NormShape& s, int es, int maps) {
     StreamPlan p = {};
     const int vec = 16 / es, row = s.C * es;
     if (s.C % vec || s.C > MAX_C || s.groups > MAX_GROUPS) return p;
-    const int ty = NC / (s.C / vec);
-    // two vectors a thread and map
-    p.srows = std::min(2 * ty, s.HW);
+    const int ty = (maps == 1 ? NC_FWD : NC_BWD) / (s.C / vec);
+    // four vectors a thread
+    p.srows = std::min(4 / maps * ty, s.HW);
     p.data = (uint32_t)p.srows * row;
     p.stage = maps * p.data + (uint32_t)(s.groups * 8 * maps + 127) / 128 * 128;
     p.stages = (int)std::min<uint32_t>(MAX_STAGES, RING / p.stage);
@@ -123,7 +122,10 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void sync_computing() { ptx::bar_sync_named(1, NC); }
+template <int NC>
+__device__ __forceinline__ void sync_computing() {
+    ptx::bar_sync_named(1, NC);
+}
 
 struct Ring {
     uint8_t* smem;
@@ -209,7 +211,7 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
     }
 }
 
-__device__ __forceinline__ Ring ring_of(const Args& a, uint8_t* smem, Header* headers, uint64_t* bars) {
+__device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t* bars, int warps) {
     Ring r;
     r.smem = smem;
     r.base = ptx::smem_u32(smem);
@@ -219,7 +221,7 @@ __device__ __forceinline__ Ring ring_of(const Args& a, uint8_t* smem, Header* he
     if (threadIdx.x == 0) {
         for (int i = 0; i < MAX_STAGES; ++i) {
             ptx::mbar_init(r.full + i * 8, 1);
-            ptx::mbar_init(r.empty + i * 8, WARPS);
+            ptx::mbar_init(r.empty + i * 8, warps);
         }
         ptx::fence_mbar_init();
     }
@@ -230,40 +232,42 @@ __device__ __forceinline__ Ring ring_of(const Args& a, uint8_t* smem, Header* he
 }
 
 // Two sums a channel of the computing threads' u and d, to red[2][slots][C]; returns slots.
-template <int V>
-__device__ __forceinline__ int spread(float (&u)[V], float (&d)[V], int tx, int ty, int cx, int ry, int C, float* red) {
+template <int P, int NC>
+__device__ __forceinline__ int spread(F2 (&u)[P], F2 (&d)[P], int tx, int ty, int cx, int ry, int C, float* red) {
     const bool pow2 = (tx & (tx - 1)) == 0 && tx < 32;
     if (pow2)
         for (int o = tx; o < 32; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                u[i] += __shfl_xor_sync(~0u, u[i], o);
-                d[i] += __shfl_xor_sync(~0u, d[i], o);
+            for (int i = 0; i < P; ++i) {
+                u[i] = u[i] + shfl_xor(u[i], o);
+                d[i] = d[i] + shfl_xor(d[i], o);
             }
-    const int slot = pow2 ? (int)threadIdx.x / 32 : ry, slots = pow2 ? WARPS : ty;
+    const int slot = pow2 ? (int)threadIdx.x / 32 : ry, slots = pow2 ? NC / 32 : ty;
     if (pow2 ? (int)(threadIdx.x % 32) < tx : ry < ty)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            red[slot * C + cx * V + i] = u[i];
-            red[(slots + slot) * C + cx * V + i] = d[i];
+        for (int i = 0; i < P; ++i) {
+            *reinterpret_cast<F2*>(&red[slot * C + (cx * P + i) * 2]) = u[i];
+            *reinterpret_cast<F2*>(&red[(slots + slot) * C + (cx * P + i) * 2]) = d[i];
         }
     return slots;
 }
 
 // After a unit's pieces are written: true in the block that finished its set.
+template <int NC>
 __device__ __forceinline__ bool last_of_set(const Args& a, int set, int* flag) {
-    sync_computing();
+    sync_computing<NC>();
     if (threadIdx.x == 0) {
         __threadfence();
         *flag = atomicAdd(a.done + set, 1) == a.p.chunks - 1;
         __threadfence();
     }
-    sync_computing();
+    sync_computing<NC>();
     return *flag;
 }
 
+template <int NC>
 __device__ __forceinline__ void release_set(const Args& a, int set) {
-    sync_computing();
+    sync_computing<NC>();
     if (threadIdx.x == 0) {
         __threadfence();
         atomicExch(a.ready + set, 1);
@@ -271,15 +275,15 @@ __device__ __forceinline__ void release_set(const Args& a, int set) {
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(NC_FWD + 32, 1)
     stream_forward_kernel(const Args a, const T* __restrict__ x, const T* __restrict__ gamma, const T* __restrict__ beta,
                           T* __restrict__ y, float* __restrict__ stats) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_FWD, WARPS = NC / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[2 * MAX_STAGES];
     __shared__ Header headers[MAX_STAGES];
     __shared__ int flag;
-    const Ring ring = ring_of(a, smem, headers, bars);
+    const Ring ring = ring_of(smem, headers, bars, NC / 32);
     if (threadIdx.x >= NC) {
         produce<T, 1>(a, ring, x, (const T*)nullptr, nullptr, true);
         return;
@@ -290,12 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int cg = s.C / s.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int tx = s.C / V, ty = NC / tx, cx = threadIdx.x % tx, ry = threadIdx.x / tx;
     const bool in = ry < ty;
-    float ga[V], be[V], k[V] = {}, u[V] = {}, d[V] = {};  // k: the unit's first pixel, or the mean
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        ga[i] = gamma ? ld1(gamma + cx * V + i) : 1.f;
-        be[i] = beta ? ld1(beta + cx * V + i) : 0.f;
-    }
+    // k: minus the unit's first pixel, or minus the mean; u, d: the sums, or rstd gamma and beta
+    F2 k[P] = {}, u[P] = {}, d[P] = {};
     float* first = red + 2 * NC * V;  // [C] the unit's first pixel
     volatile int none = 0;
     int stage = 0;
@@ -304,47 +304,50 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
-        const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage);
+        const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
         if (hd.pass == 0) {
             if (hd.first) {
-                unpack(k, q[cx]);
+                unpack(k, q[0]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    u[i] = d[i] = 0.f;
-                    if (ry == 0) first[cx * V + i] = k[i];
+                for (int i = 0; i < P; ++i) {
+                    if (ry == 0) *reinterpret_cast<F2*>(&first[(cx * P + i) * 2]) = k[i];
+                    k[i] = k[i] * f2(-1.f);
+                    u[i] = d[i] = f2(0.f);
                 }
             }
             if (in)
-#pragma unroll 2
+#pragma unroll 4
                 for (int r = ry; r < hd.n; r += ty) {
-                    float v[V];
-                    unpack(v, q[r * tx + cx]);
+                    F2 v[P];
+                    unpack(v, q[r * tx]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float e = v[i] - k[i];
-                        u[i] += e;
-                        d[i] = fmaf(e, e, d[i]);
+                    for (int i = 0; i < P; ++i) {
+                        const F2 e = v[i] + k[i];
+                        u[i] = u[i] + e;
+                        d[i] = fma(e, e, d[i]);
                     }
                 }
         } else {
-            if (hd.first) {  // u: rstd gamma
+            if (hd.first) {
                 const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + p.data);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 v = st[(cx * V + i) / cg];
-                    k[i] = v.x;
-                    u[i] = v.y * ga[i];
+                for (int i = 0; i < P; ++i) {
+                    const int c = (cx * P + i) * 2;
+                    const float2 v = st[c / cg], w = st[(c + 1) / cg];
+                    k[i] = f2(-v.x, -w.x);
+                    u[i] = f2(v.y * (gamma ? ld1(gamma + c) : 1.f), w.y * (gamma ? ld1(gamma + c + 1) : 1.f));
+                    d[i] = f2(beta ? ld1(beta + c) : 0.f, beta ? ld1(beta + c + 1) : 0.f);
                 }
             }
             if (in) {
                 T* yp = y + ((size_t)hd.set * s.HW + hd.row0) * s.C + cx * V;
-#pragma unroll 2
+#pragma unroll 4
                 for (int r = ry; r < hd.n; r += ty) {
-                    float v[V];
-                    unpack(v, q[r * tx + cx]);
+                    F2 v[P];
+                    unpack(v, q[r * tx]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = act_apply<ACT, kFast<T>>(fmaf(v[i] - k[i], u[i], be[i]));
-                    *reinterpret_cast<uint4*>(yp + (size_t)r * s.C) = pack<T>(v);
+                    for (int i = 0; i < P; ++i) v[i] = act_apply<ACT, kFast<T>>(fma(v[i] + k[i], u[i], d[i]));
+                    *reinterpret_cast<uint4*>(yp + (size_t)r * s.C) = pack(v);
                 }
             }
         }
@@ -352,8 +355,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (hd.pass == 0 && hd.last) {
-            const int slots = spread<V>(u, d, tx, ty, cx, ry, s.C, red);
-            sync_computing();
+            const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
+            sync_computing<NC>();
             const float n = (float)(min((hd.chunk + 1) * p.rows, s.HW) - hd.chunk * p.rows);
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 red[c] = first[c] + m;
                 red[slots * s.C + c] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
             }
-            sync_computing();
+            sync_computing<NC>();
             for (int g = warp; g < s.groups; g += WARPS) {
                 float e = 0.f;
                 for (int c = lane; c < cg; c += 32) e += red[g * cg + c];
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0)
                     a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.groups + g] = make_float2(mean, m2);
             }
-            if (last_of_set(a, hd.set, &flag)) {
+            if (last_of_set<NC>(a, hd.set, &flag)) {
                 const float total = (float)s.HW * (float)cg;
                 auto count = [&](int i) { return (float)(min((i + 1) * p.rows, s.HW) - i * p.rows) * (float)cg; };
                 for (int g = warp; g < s.groups; g += WARPS) {
@@ -405,23 +408,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                release_set(a, hd.set);
+                release_set<NC>(a, hd.set);
             }
         }
     }
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(NC_BWD + 32, 1)
     stream_backward_kernel(const Args a, const T* __restrict__ x, const T* __restrict__ gamma,
                            const T* __restrict__ beta, const float* __restrict__ stats, const T* __restrict__ gy,
                            T* __restrict__ gx, float* __restrict__ gg, float* __restrict__ gb) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_BWD, WARPS = NC / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[2 * MAX_STAGES];
     __shared__ Header headers[MAX_STAGES];
     __shared__ int flag;
-    const Ring ring = ring_of(a, smem, headers, bars);
+    const Ring ring = ring_of(smem, headers, bars, NC / 32);
     if (threadIdx.x >= NC) {
         produce<T, 2>(a, ring, x, gy, stats, gx != nullptr);
         return;
@@ -434,11 +437,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool in = ry < ty;
     float2* csums = a.sets;                    // [B][C] sums of a sample's channels
     float2* c12 = a.sets + (size_t)s.B * s.C;  // [B][groups] (c1, c2)
-    float ga[V], be[V], mean[V] = {}, rstd[V] = {}, u[V] = {}, d[V] = {};  // u, d: the sums, or c1 and c2
+    Channels<P> ch = {};
+    F2 u[P] = {}, d[P] = {};  // the sums, or -c1 and -c2
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        ga[i] = gamma ? ld1(gamma + cx * V + i) : 1.f;
-        be[i] = beta ? ld1(beta + cx * V + i) : 0.f;
+    for (int i = 0; i < P; ++i) {
+        const int c = (cx * P + i) * 2;
+        ch.ga[i] = f2(gamma ? ld1(gamma + c) : 1.f, gamma ? ld1(gamma + c + 1) : 1.f);
+        ch.be[i] = f2(beta ? ld1(beta + c) : 0.f, beta ? ld1(beta + c + 1) : 0.f);
     }
     volatile int none = 0;
     int stage = 0;
@@ -447,51 +452,58 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
-        const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage);
-        const uint4* h = reinterpret_cast<const uint4*>(smem + stage * p.stage + p.data);
+        const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
+        const uint4* h = reinterpret_cast<const uint4*>(smem + stage * p.stage + p.data) + cx;
         if (hd.first) {
             const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + 2 * p.data);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int g = (cx * V + i) / cg;
-                const float2 v = st[g];
-                mean[i] = v.x;
-                rstd[i] = v.y;
-                u[i] = d[i] = 0.f;
+            for (int i = 0; i < P; ++i) {
+                const int g0 = (cx * P + i) * 2 / cg, g1 = ((cx * P + i) * 2 + 1) / cg;
+                const float2 v = st[g0], w = st[g1];
+                ch.nmean[i] = f2(-v.x, -w.x);
+                ch.rstd[i] = f2(v.y, w.y);
+                u[i] = d[i] = f2(0.f);
                 if (hd.pass == 1) {
-                    const float2 w = st[s.groups + g];
-                    u[i] = w.x;
-                    d[i] = w.y;
+                    const float2 e = st[s.groups + g0], f = st[s.groups + g1];
+                    u[i] = f2(-e.x, -f.x);
+                    d[i] = f2(-e.y, -f.y);
                 }
             }
         }
         if (in) {
-            T* gp = gx + ((size_t)hd.set * s.HW + hd.row0) * s.C + cx * V;
+            if (hd.pass == 0) {
 #pragma unroll 2
-            for (int r = ry; r < hd.n; r += ty) {
-                float v[V], g[V];
-                unpack(v, q[r * tx + cx]);
-                unpack(g, h[r * tx + cx]);
+                for (int r = ry; r < hd.n; r += ty) {
+                    F2 v[P], g[P], dz[P], hat[P];
+                    unpack(v, q[r * tx]);
+                    unpack(g, h[r * tx]);
+                    ch.template dz<ACT, kFast<T>>(v, g, dz, hat);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float hat = (v[i] - mean[i]) * rstd[i];
-                    const float dz = dz_of<ACT, kFast<T>>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
-                    if (hd.pass == 0) {
-                        u[i] += dz;
-                        d[i] = fmaf(dz, hat, d[i]);
-                    } else {
-                        v[i] = rstd[i] * (fmaf(ga[i], dz, -u[i]) - hat * d[i]);
+                    for (int i = 0; i < P; ++i) {
+                        u[i] = u[i] + dz[i];
+                        d[i] = fma(dz[i], hat[i], d[i]);
                     }
                 }
-                if (hd.pass == 1) *reinterpret_cast<uint4*>(gp + (size_t)r * s.C) = pack<T>(v);
+            } else {
+                T* gp = gx + ((size_t)hd.set * s.HW + hd.row0) * s.C + cx * V;
+#pragma unroll 2
+                for (int r = ry; r < hd.n; r += ty) {
+                    F2 v[P], g[P], dz[P], hat[P];
+                    unpack(v, q[r * tx]);
+                    unpack(g, h[r * tx]);
+                    ch.template dz<ACT, kFast<T>>(v, g, dz, hat);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) v[i] = ch.rstd[i] * fma(hat[i], d[i], fma(ch.ga[i], dz[i], u[i]));
+                    *reinterpret_cast<uint4*>(gp + (size_t)r * s.C) = pack(v);
+                }
             }
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (hd.pass == 0 && hd.last) {
-            const int slots = spread<V>(u, d, tx, ty, cx, ry, s.C, red);
-            sync_computing();
+            const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
+            sync_computing<NC>();
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
 #pragma unroll 8
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.C + c] = make_float2(e, f);
             }
-            if (last_of_set(a, hd.set, &flag)) {
+            if (last_of_set<NC>(a, hd.set, &flag)) {
                 for (int c = threadIdx.x; c < s.C; c += NC) {
                     float2 v = make_float2(0.f, 0.f);
 #pragma unroll 8
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     red[c] = k * v.x;
                     red[s.C + c] = k * v.y;
                 }
-                sync_computing();
+                sync_computing<NC>();
                 const float inv = 1.f / ((float)s.HW * (float)cg);
                 for (int g = warp; g < s.groups; g += WARPS) {
                     float e = 0.f, f = 0.f;
@@ -527,13 +539,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     f = warp_sum(f);
                     if (lane == 0) c12[(size_t)hd.set * s.groups + g] = make_float2(e * inv, f * inv);
                 }
-                release_set(a, hd.set);
+                release_set<NC>(a, hd.set);
                 if (gg || gb) {  // the last set of all sums the parameters' gradients
                     if (threadIdx.x == 0) {
                         flag = atomicAdd(a.finished, 1) == s.B - 1;
                         __threadfence();
                     }
-                    sync_computing();
+                    sync_computing<NC>();
                     if (flag)
                         for (int c = threadIdx.x; c < s.C; c += NC) params_of(s, csums, c, gg, gb);
                 }
@@ -543,13 +555,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <typename F, typename... Q>
-cudaError_t launch(F f, DeviceFlags& flags, const Args& a, cudaStream_t st, Q... args) {
+cudaError_t launch(F f, DeviceFlags& flags, int threads, const Args& a, cudaStream_t st, Q... args) {
     const uint32_t bytes = a.p.stages * a.p.stage + RED_BYTES + MAX_C * 4;
     cudaError_t e = max_dynamic_smem_once((const void*)f, RING + RED_BYTES + MAX_C * 4, flags);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.p.grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -580,7 +592,7 @@ template <typename T>
 cudaError_t forward_t(const Args& a, const T* x, const T* gamma, const T* beta, T* y, float* stats, cudaStream_t st) {
     return with_act(a.s.act, [&](auto A) {
         static DeviceFlags flags;
-        return launch(stream_forward_kernel<T, decltype(A)::value>, flags, a, st, x, gamma, beta, y, stats);
+        return launch(stream_forward_kernel<T, decltype(A)::value>, flags, NC_FWD + 32, a, st, x, gamma, beta, y, stats);
     });
 }
 
@@ -589,7 +601,8 @@ cudaError_t backward_t(const Args& a, const T* x, const T* gamma, const T* beta,
                        float* gg, float* gb, cudaStream_t st) {
     return with_act(a.s.act, [&](auto A) {
         static DeviceFlags flags;
-        return launch(stream_backward_kernel<T, decltype(A)::value>, flags, a, st, x, gamma, beta, stats, gy, gx, gg, gb);
+        return launch(stream_backward_kernel<T, decltype(A)::value>, flags, NC_BWD + 32, a, st, x, gamma, beta, stats, gy, gx,
+                      gg, gb);
     });
 }
 
