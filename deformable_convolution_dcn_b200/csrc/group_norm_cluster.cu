@@ -96,18 +96,18 @@ struct Lanes {
 
 // Sums per channel over the block's threads of `a`, to red[slot][cb]; returns the number of slots. Where a warp
 // holds whole rows of vectors its lanes add up first.
-template <int V, int NT>
-__device__ __forceinline__ int spread_sums(float (&a)[V], const Lanes& l, int cb, float* red) {
+template <int P, int NT>
+__device__ __forceinline__ int spread_sums(F2 (&a)[P], const Lanes& l, int cb, float* red) {
     const bool pow2 = (l.tx & (l.tx - 1)) == 0 && l.tx < 32;
     if (pow2) {
         for (int o = l.tx; o < 32; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < V; ++i) a[i] += __shfl_xor_sync(~0u, a[i], o);
+            for (int i = 0; i < P; ++i) a[i] = a[i] + shfl_xor(a[i], o);
     }
     const int slot = pow2 ? (int)threadIdx.x / 32 : l.ry;
     if (pow2 ? (int)(threadIdx.x % 32) < l.tx : l.ry < l.ty)
 #pragma unroll
-        for (int i = 0; i < V; ++i) red[slot * cb + l.cx * V + i] = a[i];
+        for (int i = 0; i < P; ++i) *reinterpret_cast<F2*>(&red[slot * cb + (l.cx * P + i) * 2]) = a[i];
     return pow2 ? NT / 32 : l.ty;
 }
 
@@ -128,7 +128,7 @@ template <typename T, int ACT>
 __global__ void __launch_bounds__(NT_FWD, 2)
     cluster_forward_kernel(const NormShape s, const ClusterPlan p, const T* __restrict__ x, const T* __restrict__ gamma,
                            const T* __restrict__ beta, T* __restrict__ y, float* __restrict__ stats) {
-    constexpr int V = 16 / (int)sizeof(T), NT = NT_FWD;
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NT = NT_FWD;
     extern __shared__ __align__(16) uint8_t smem[];
     uint4* slab = reinterpret_cast<uint4*>(smem);
     float* red = reinterpret_cast<float*>(smem + p.slab);
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(NT_FWD, 2)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const T* xp = x + ((size_t)b * s.HW + r0) * s.C + c0 + l.cx * V;
-    float a[V] = {};
+    F2 a[P] = {};
     if (in) {
         int r = l.ry;
         for (; r + 7 * l.ty < n; r += 8 * l.ty) {
@@ -155,52 +155,56 @@ __global__ void __launch_bounds__(NT_FWD, 2)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 slab[(r + k * l.ty) * l.tx + l.cx] = q[k];
-                float v[V];
+                F2 v[P];
                 unpack(v, q[k]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) a[i] += v[i];
+                for (int i = 0; i < P; ++i) a[i] = a[i] + v[i];
             }
         }
 #pragma unroll 4
         for (; r < n; r += l.ty) {
             const uint4 q = ptx::ldg_v4_stream(xp + (size_t)r * s.C);
             slab[r * l.tx + l.cx] = q;
-            float v[V];
+            F2 v[P];
             unpack(v, q);
 #pragma unroll
-            for (int i = 0; i < V; ++i) a[i] += v[i];
+            for (int i = 0; i < P; ++i) a[i] = a[i] + v[i];
         }
     }
     // gamma and beta on their way while the sums are joined
-    float ga[V], be[V];
+    F2 ga[P], be[P];
+    int g0[P], g1[P];  // the pairs' groups
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        ga[i] = gamma && in ? ld1(gamma + c0 + l.cx * V + i) : 1.f;
-        be[i] = beta && in ? ld1(beta + c0 + l.cx * V + i) : 0.f;
+    for (int i = 0; i < P; ++i) {
+        const int c = (l.cx * P + i) * 2;
+        ga[i] = f2(gamma && in ? ld1(gamma + c0 + c) : 1.f, gamma && in ? ld1(gamma + c0 + c + 1) : 1.f);
+        be[i] = f2(beta && in ? ld1(beta + c0 + c) : 0.f, beta && in ? ld1(beta + c0 + c + 1) : 0.f);
+        g0[i] = c / cg;
+        g1[i] = (c + 1) / cg;
     }
-    int slots = spread_sums<V, NT>(a, l, cb, red);
+    int slots = spread_sums<P, NT>(a, l, cb, red);
     __syncthreads();
     group_sums<NT>(red, slots, cb, cg, ng, lmean);
     __syncthreads();
     const float inv = n > 0 ? 1.f / ((float)n * (float)cg) : 0.f;
-    float m[V];
+    F2 m[P];  // minus the mean
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        m[i] = lmean[(l.cx * V + i) / cg] * inv;
-        a[i] = 0.f;
+    for (int i = 0; i < P; ++i) {
+        m[i] = f2(-lmean[g0[i]] * inv, -lmean[g1[i]] * inv);
+        a[i] = f2(0.f);
     }
     if (in)
 #pragma unroll 4
         for (int r = l.ry; r < n; r += l.ty) {
-            float v[V];
+            F2 v[P];
             unpack(v, slab[r * l.tx + l.cx]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = v[i] - m[i];
-                a[i] = fmaf(d, d, a[i]);
+            for (int i = 0; i < P; ++i) {
+                const F2 d = v[i] + m[i];
+                a[i] = fma(d, d, a[i]);
             }
         }
-    slots = spread_sums<V, NT>(a, l, cb, red);
+    slots = spread_sums<P, NT>(a, l, cb, red);
     __syncthreads();
     group_sums<NT>(red, slots, cb, cg, ng, lm2);
     // the cluster's runs joined: counts are known, means and squares about them come from each CTA
@@ -240,22 +244,20 @@ __global__ void __launch_bounds__(NT_FWD, 2)
     __syncthreads();
     // this CTA has read the others' sums: they may leave (waited for at the end)
     if (p.cs > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    float sc[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int g = (l.cx * V + i) / cg;
-        m[i] = gmean[g];
-        sc[i] = grstd[g] * ga[i];
+    for (int i = 0; i < P; ++i) {
+        m[i] = f2(-gmean[g0[i]], -gmean[g1[i]]);
+        ga[i] = ga[i] * f2(grstd[g0[i]], grstd[g1[i]]);
     }
     if (in) {
         T* yp = y + ((size_t)b * s.HW + r0) * s.C + c0 + l.cx * V;
 #pragma unroll 4
         for (int r = l.ry; r < n; r += l.ty) {
-            float v[V];
+            F2 v[P];
             unpack(v, slab[r * l.tx + l.cx]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = act_apply<ACT, kFast<T>>(fmaf(v[i] - m[i], sc[i], be[i]));
-            *reinterpret_cast<uint4*>(yp + (size_t)r * s.C) = pack<T>(v);
+            for (int i = 0; i < P; ++i) v[i] = act_apply<ACT, kFast<T>>(fma(v[i] + m[i], ga[i], be[i]));
+            *reinterpret_cast<uint4*>(yp + (size_t)r * s.C) = pack(v);
         }
     }
     if (p.cs > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(NT_BWD, 2)
     cluster_backward_kernel(const NormShape s, const ClusterPlan p, const T* __restrict__ x, const T* __restrict__ gamma,
                             const T* __restrict__ beta, const float* __restrict__ stats, const T* __restrict__ gy,
                             float2* __restrict__ sums, T* __restrict__ gx) {
-    constexpr int V = 16 / (int)sizeof(T), NT = NT_BWD;
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NT = NT_BWD;
     extern __shared__ __align__(16) uint8_t smem[];
     uint4* slab = reinterpret_cast<uint4*>(smem);
     uint4* slab2 = reinterpret_cast<uint4*>(smem + p.slab);
@@ -282,27 +284,31 @@ __global__ void __launch_bounds__(NT_BWD, 2)
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    float mean[V], rstd[V], ga[V], be[V], s1[V] = {}, s2[V] = {};
+    Channels<P> ch;
+    F2 s1[P] = {}, s2[P] = {};
+    int g0[P], g1[P];  // the pairs' groups within the block
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int ch = c0 + l.cx * V + i;
-        const float* st = stats + ((size_t)b * s.groups + ch / cg) * 2;
-        mean[i] = __ldg(st);
-        rstd[i] = __ldg(st + 1);
-        ga[i] = gamma ? ld1(gamma + ch) : 1.f;
-        be[i] = beta ? ld1(beta + ch) : 0.f;
+    for (int i = 0; i < P; ++i) {
+        const int c = (l.cx * P + i) * 2;
+        g0[i] = c / cg;
+        g1[i] = (c + 1) / cg;
+        const float* st = stats + ((size_t)b * s.groups + c0 / cg) * 2;
+        ch.nmean[i] = f2(-__ldg(st + 2 * g0[i]), -__ldg(st + 2 * g1[i]));
+        ch.rstd[i] = f2(__ldg(st + 2 * g0[i] + 1), __ldg(st + 2 * g1[i] + 1));
+        ch.ga[i] = f2(gamma ? ld1(gamma + c0 + c) : 1.f, gamma ? ld1(gamma + c0 + c + 1) : 1.f);
+        ch.be[i] = f2(beta ? ld1(beta + c0 + c) : 0.f, beta ? ld1(beta + c0 + c + 1) : 0.f);
     }
+    ch.set_border();
     const size_t at = ((size_t)b * s.HW + r0) * s.C + c0 + l.cx * V;
     auto take = [&](const uint4& qx, const uint4& qg) {
-        float v[V], g[V];
+        F2 v[P], g[P], dz[P], hat[P];
         unpack(v, qx);
         unpack(g, qg);
+        ch.template dz<ACT, kFast<T>>(v, g, dz, hat);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float hat = (v[i] - mean[i]) * rstd[i];
-            const float d = dz_of<ACT, kFast<T>>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
-            s1[i] += d;
-            s2[i] = fmaf(d, hat, s2[i]);
+        for (int i = 0; i < P; ++i) {
+            s1[i] = s1[i] + dz[i];
+            s2[i] = fma(dz[i], hat[i], s2[i]);
         }
     };
     if (in) {
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(NT_BWD, 2)
     }
     // sums of a channel over the CTA
     for (int k = 0; k < 2; ++k) {
-        const int slots = spread_sums<V, NT>(k ? s2 : s1, l, cb, red);
+        const int slots = spread_sums<P, NT>(k ? s2 : s1, l, cb, red);
         __syncthreads();
         for (int c = threadIdx.x; c < cb; c += NT) {
             float v = 0.f;
@@ -366,25 +372,21 @@ __global__ void __launch_bounds__(NT_BWD, 2)
         }
         __syncthreads();
         if (in) {
-            float c1[V], c2[V];
+            F2 c1[P], c2[P];  // negated
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int g = (l.cx * V + i) / cg;
-                c1[i] = red[g];
-                c2[i] = red[MAX_CB + g];
+            for (int i = 0; i < P; ++i) {
+                c1[i] = f2(-red[g0[i]], -red[g1[i]]);
+                c2[i] = f2(-red[MAX_CB + g0[i]], -red[MAX_CB + g1[i]]);
             }
 #pragma unroll 2
             for (int r = l.ry; r < n; r += l.ty) {
-                float v[V], g[V];
+                F2 v[P], g[P], dz[P], hat[P];
                 unpack(v, slab[r * l.tx + l.cx]);
                 unpack(g, slab2[r * l.tx + l.cx]);
+                ch.template dz<ACT, kFast<T>>(v, g, dz, hat);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float hat = (v[i] - mean[i]) * rstd[i];
-                    const float d = dz_of<ACT, kFast<T>>(g[i], v[i], hat, mean[i], rstd[i], ga[i], be[i]);
-                    v[i] = rstd[i] * (fmaf(ga[i], d, -c1[i]) - hat * c2[i]);
-                }
-                *reinterpret_cast<uint4*>(gx + at + (size_t)r * s.C) = pack<T>(v);
+                for (int i = 0; i < P; ++i) v[i] = ch.rstd[i] * fma(hat[i], c2[i], fma(ch.ga[i], dz[i], c1[i]));
+                *reinterpret_cast<uint4*>(gx + at + (size_t)r * s.C) = pack(v);
             }
         }
     }

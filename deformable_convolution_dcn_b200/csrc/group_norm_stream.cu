@@ -1,18 +1,19 @@
 // Group normalisation with an activation, channels last, for long maps of whole
-// vectors: the queue of group_norm.cu (units summed first and applied a few sets
-// later, from L2) with the loads taken off the threads that compute.
+// vectors: a queue of units as in group_norm.cu (all summed first, then applied; what
+// L2 still holds by then is not read again from HBM), with the loads taken off the
+// threads that compute.
 //
-// One block an SM. A producer warp claims the units and copies their pixels, which
-// lie in one run, to a ring of shared-memory stages (bulk copies, up to 150 KB in
-// flight); the other warps compute from there and store. So the memory works on while
-// a unit's sums are reduced, joined and released, and those latencies, which bound
-// the kernels without the ring (8x200x200x128: 92 us), cost nothing. The producer
-// also waits for a set's statistics before it copies a unit of the second pass, and
-// leaves them in the unit's first stage.
+// One block an SM. A producer warp claims the units and copies their pixels, in runs
+// of one stage, to a ring of shared-memory stages (bulk copies, up to 160 KB in
+// flight); most warps compute from there and store; four more warps count the summed
+// units and join their sets. So the memory works on while sums are counted, joined and
+// released, and those latencies cost little: with the fence and the atomic in a
+// computing warp a unit cost nine microseconds more, in a kernel without the ring
+// (group_norm.cu) 8x200x200x128 takes 92 us. The producer waits for a set's statistics
+// before it copies a unit of the second pass, and leaves them in its first stage.
 //
 // A claimed unit waits for none but lower ones, which are summed by blocks that
-// never wait (see group_norm.cu); the end of a set's sums is looked at before the
-// next stage is waited for, so no block's own next unit can hold it up.
+// never wait (see group_norm.cu), and the warps that join wait for no unit.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,8 +25,9 @@
 namespace dcn {
 namespace {
 
-// computing threads (and a producer warp): the backward keeps twice the parameters in registers
-constexpr int NC_FWD = 768, NC_BWD = 512;
+// computing threads: the backward keeps twice the parameters in registers
+constexpr int NC_FWD = 608, NC_BWD = 448;
+constexpr int JOINERS = 128;             // threads that join, after the producer warp
 constexpr int MAX_STAGES = 16;
 constexpr int MAX_C = 1024;
 constexpr int MAX_GROUPS = 256;          // their statistics travel in a stage
@@ -35,10 +37,10 @@ constexpr long long WAIT_LIMIT = 2000000000LL;
 
 struct StreamPlan {
     bool ok;
-    int rows, chunks;      // pixels a unit, units a set (a sample)
+    int chunks, blocks;    // units of a set (a sample), runs of srows pixels: unit i has the runs i, i + chunks, ...
     int srows, stages;     // pixels a stage, stages
     uint32_t data, stage;  // bytes of one map's pixels, of a stage
-    int lag, grid;
+    int grid;
 };
 
 StreamPlan stream_plan(const NormShape& s, int es, int maps) {
@@ -49,17 +51,14 @@ StreamPlan stream_plan(const NormShape& s, int es, int maps) {
     // four vectors a thread
     p.srows = std::min(4 / maps * ty, s.HW);
     p.data = (uint32_t)p.srows * row;
-    p.stage = maps * p.data + (uint32_t)(s.groups * 8 * maps + 127) / 128 * 128;
+    p.stage = (maps * (p.data + s.groups * 8) + 127) / 128 * 128;
     p.stages = (int)std::min<uint32_t>(MAX_STAGES, RING / p.stage);
-    // units of 256 KB: their reduction takes about as long as their pixels' way from HBM; smaller ones where the map
-    // would not give every SM two
-    long long rows = std::max<long long>(1, 256 * 1024 / ((long long)row * maps));
-    rows = std::min(rows, std::max<long long>(1, (long long)s.HW * s.B / 296));
-    rows = std::max<long long>((rows + p.srows - 1) / p.srows, 1) * p.srows;
-    rows = std::max(rows, (s.HW + 255LL) / 256);  // the join walks at most 256 units
-    p.rows = (int)std::min<long long>(rows, s.HW);
-    p.chunks = (s.HW + p.rows - 1) / p.rows;
-    p.lag = (int)std::min<long long>(s.B, 296 / p.chunks + 2);
+    // A unit costs a few microseconds beside its pixels (reduction, join, wait), so the sets are cut in as many units as
+    // there are SMs and no more: 8x100x100x256 backward takes 58 us, with twice the units, which L2 would hold until
+    // their second pass, 74 us; forward the two are even (8x200x200x128 without activation: 51.5 and 49.5 us).
+    const int chunks = s.B <= 74 ? 148 / s.B : s.B < 148 ? 2 : 1;
+    p.blocks = (s.HW + p.srows - 1) / p.srows;
+    p.chunks = std::min(chunks, p.blocks);
     p.grid = (int)std::min<long long>(148, (long long)s.B * p.chunks);
     p.ok = true;
     return p;
@@ -86,34 +85,25 @@ struct Args {
 };
 
 // What the producer says of a stage.
-struct Header {
-    int pass;   // 0 sums, 1 applies, -1: no more units
+struct __align__(16) Header {
+    int pass;   // 0 sums, 1 applies, -1: no more units; + 4: the unit's first stage, + 8: its last
     int set, chunk;
-    int row0, n;  // its pixels, within the sample
-    int first, last;
+    int row0;   // its pixels, srows or up to the end of the sample
 };
 
-// As in group_norm.cu: unit t of the queue.
+// The queue: every set's units summed, then every set's applied.
 __device__ __forceinline__ void unit_at(const Args& a, int t, int& pass, int& set, int& chunk) {
-    const int U = a.p.chunks, Q = a.s.B, L = a.p.lag;
-    if (t < L * U) {
-        pass = 0;
-        set = t / U;
-        chunk = t % U;
-        return;
-    }
-    int r = t - L * U;
-    if (r < (Q - L) * 2 * U) {
-        const int i = r / (2 * U), w = r % (2 * U);
-        pass = w >= U;
-        set = pass ? i : L + i;
-        chunk = pass ? w - U : w;
-        return;
-    }
-    r -= (Q - L) * 2 * U;
-    pass = 1;
-    set = Q - L + r / U;
-    chunk = r % U;
+    const int half = a.s.B * a.p.chunks;
+    pass = t >= half;
+    set = (t - pass * half) / a.p.chunks;
+    chunk = t % a.p.chunks;
+}
+
+// Pixels of a set's unit i.
+__device__ __forceinline__ int pixels_of(const Args& a, int i) {
+    const int runs = (a.p.blocks - 1 - i) / a.p.chunks + 1;
+    const bool last = (a.p.blocks - 1) % a.p.chunks == i;
+    return runs * a.p.srows - (last ? a.p.blocks * a.p.srows - a.s.HW : 0);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -127,13 +117,33 @@ __device__ __forceinline__ void sync_computing() {
     ptx::bar_sync_named(1, NC);
 }
 
+// Waits, a warp, until the set's sums are joined; false when the bounded wait ran out.
+__device__ __forceinline__ bool await_set(const Args& a, int set) {
+    bool ok = true;
+    if (ptx::ld_acquire_gpu(a.ready + set) == 0) {
+        const long long t0 = clock64();
+        while (ptx::ld_acquire_gpu(a.ready + set) == 0) {
+            __nanosleep(100);
+            if (clock64() - t0 > WAIT_LIMIT) {
+                atomicOr(a.status, ptx::kStatusTimeout);
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(~0u, ok);
+}
+
 struct Ring {
     uint8_t* smem;
     uint32_t base, full, empty;  // shared addresses: stages, barriers
     Header* headers;
+    // summed units on their way to the joining warps, in two slots: the set (-1: no more), its barriers
+    int* unit_set;
+    uint32_t unit_done, unit_free;
 };
 
-// The producer warp. maps: x, or x and grad_y; apply: the second pass is wanted; stats: (mean, rstd) of the backward.
+// The producer warp. MAPS: x, or x and grad_y; stats: the backward's (mean, rstd); apply: the second pass is wanted.
 template <typename T, int MAPS>
 __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T* x, const T* gy, const float* stats,
                                         bool apply) {
@@ -146,39 +156,25 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
     uint32_t phase = 1;
     volatile int none = 0;
     bool ok = true;
-    int claim = 0;
-    if (lane == 0) claim = atomicAdd(a.ticket, 1);
+    // Claimed when the unit before is on its way, not earlier: the ring hides the answer's time, and a unit held by a
+    // block that is not at it is one that an idle block misses.
     for (;;) {
-        const int t = __shfl_sync(~0u, claim, 0);
+        int t = 0;
+        if (lane == 0) t = atomicAdd(a.ticket, 1);
+        t = __shfl_sync(~0u, t, 0);
         if (t >= total || !ok) break;
-        if (lane == 0) claim = atomicAdd(a.ticket, 1);  // the unit after: answered meanwhile
         int pass, set, chunk;
-        if (apply) {
-            unit_at(a, t, pass, set, chunk);
-        } else {
-            pass = 0;
-            set = t / p.chunks;
-            chunk = t % p.chunks;
-        }
+        unit_at(a, t, pass, set, chunk);
         if (pass == 1) {  // the set's sums are joined
-            const long long t0 = clock64();
-            while (ptx::ld_acquire_gpu(a.ready + set) == 0) {
-                __nanosleep(100);
-                if (clock64() - t0 > WAIT_LIMIT) {
-                    atomicOr(a.status, ptx::kStatusTimeout);
-                    ok = false;
-                    break;
-                }
-            }
-            ok = __all_sync(~0u, ok);
+            ok = await_set(a, set);
             if (!ok) break;
         }
-        const int r0 = chunk * p.rows, r1 = min(r0 + p.rows, s.HW);
-        for (int r = r0; r < r1; r += p.srows) {
+        for (int k = chunk; k < p.blocks; k += p.chunks) {
+            const int r = k * p.srows;
             ok = __all_sync(~0u, ptx::mbar_wait(ring.empty + stage * 8, phase, &none, a.status, WAIT_LIMIT));
             if (!ok) break;
-            const int n = min(p.srows, r1 - r);
-            if (r == r0) {  // the statistics that the unit needs
+            const int n = min(p.srows, s.HW - r);
+            if (k == chunk) {  // the statistics that the unit needs
                 float2* st = reinterpret_cast<float2*>(ring.smem + stage * p.stage + MAPS * p.data);
                 for (int g = lane; g < s.groups; g += 32) {
                     if (MAPS == 2) {
@@ -192,7 +188,7 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
             }
             __syncwarp();
             if (lane == 0) {
-                ring.headers[stage] = Header{pass, set, chunk, r, n, r == r0, r + p.srows >= r1};
+                ring.headers[stage] = Header{pass | (k == chunk ? 4 : 0) | (k + p.chunks >= p.blocks ? 8 : 0), set, chunk, r};
                 const uint32_t bytes = n * row, dst = ring.base + stage * p.stage, bar = ring.full + stage * 8;
                 ptx::mbar_arrive_expect_tx(bar, MAPS * bytes);
                 const size_t at = ((size_t)set * s.HW + r) * s.C;
@@ -211,14 +207,21 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
     }
 }
 
-__device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t* bars, int warps) {
+__device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t* bars, int* unit_set, int warps) {
     Ring r;
     r.smem = smem;
     r.base = ptx::smem_u32(smem);
     r.headers = headers;
     r.full = ptx::smem_u32(bars);
     r.empty = r.full + MAX_STAGES * 8;
+    r.unit_set = unit_set;
+    r.unit_done = r.empty + MAX_STAGES * 8;
+    r.unit_free = r.unit_done + 16;
     if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(r.unit_done + i * 8, warps);
+            ptx::mbar_init(r.unit_free + i * 8, 1);
+        }
         for (int i = 0; i < MAX_STAGES; ++i) {
             ptx::mbar_init(r.full + i * 8, 1);
             ptx::mbar_init(r.empty + i * 8, warps);
@@ -252,38 +255,115 @@ __device__ __forceinline__ int spread(F2 (&u)[P], F2 (&d)[P], int tx, int ty, in
     return slots;
 }
 
-// After a unit's pieces are written: true in the block that finished its set.
-template <int NC>
-__device__ __forceinline__ bool last_of_set(const Args& a, int set, int* flag) {
-    sync_computing<NC>();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        *flag = atomicAdd(a.done + set, 1) == a.p.chunks - 1;
-        __threadfence();
+// The computing warps' side of the way to the joining warps.
+struct Post {
+    int n = 0;
+    // The unit's pieces are written by this thread; set -1: no more units. All computing threads.
+    __device__ __forceinline__ void operator()(const Args& a, const Ring& ring, int set) {
+        const int slot = n & 1;
+        volatile int none = 0;
+        if (threadIdx.x == 0) {  // the slot's unit before the last has been taken
+            if (n >= 2) ptx::mbar_wait(ring.unit_free + slot * 8, ((n >> 1) - 1) & 1, &none, a.status, WAIT_LIMIT);
+            ring.unit_set[slot] = set;
+        }
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) ptx::mbar_arrive(ring.unit_done + slot * 8);
+        ++n;
     }
-    sync_computing<NC>();
-    return *flag;
+};
+
+__device__ __forceinline__ void sync_joiners() { ptx::bar_sync_named(2, JOINERS); }
+
+// The joining warps: counts each summed unit in its set, and join(set) for the sets that this block has finished.
+template <typename F>
+__device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* flag, F&& join) {
+    const bool head = threadIdx.x % 32 == 0 && (int)threadIdx.x == (int)blockDim.x - JOINERS;
+    volatile int none = 0;
+    for (int n = 0;; ++n) {
+        const int slot = n & 1;
+        // a unit may be a long time away (the wait of the producer among the reasons): no limit but the kernel's own end
+        if (!ptx::mbar_wait(ring.unit_done + slot * 8, (n >> 1) & 1, &none, a.status, 4 * WAIT_LIMIT)) return;
+        const int set = ring.unit_set[slot];
+        if (set < 0) return;
+        sync_joiners();
+        if (head) {
+            ptx::mbar_arrive(ring.unit_free + slot * 8);
+            __threadfence();
+            *flag = atomicAdd(a.done + set, 1) == a.p.chunks - 1;
+            __threadfence();
+        }
+        sync_joiners();
+        if (*flag) {
+            join(set);
+            sync_joiners();  // all of it is written
+            if (head) {
+                __threadfence();
+                atomicExch(a.ready + set, 1);
+            }
+        }
+    }
 }
 
-template <int NC>
-__device__ __forceinline__ void release_set(const Args& a, int set) {
-    sync_computing<NC>();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicExch(a.ready + set, 1);
+// The forward's join: mean and rstd of a set's groups. Four threads share a group's units; sums are taken about the
+// first unit's mean.
+__device__ __forceinline__ void join_stats(const Args& a, int set, float* stats, float4* sm) {
+    const NormShape& s = a.s;
+    const StreamPlan& p = a.p;
+    const int t = threadIdx.x - (blockDim.x - JOINERS), cg = s.C / s.groups;
+    const float total = (float)s.HW * (float)cg;
+    for (int base = 0; base < s.groups; base += 32) {
+        const int g = base + t % 32, part = t / 32;
+        float u = 0.f, sq = 0.f, m2 = 0.f, first = 0.f;
+        if (g < s.groups) {
+            const float2* pc = a.pieces + (size_t)set * p.chunks * s.groups + g;
+            first = __ldcg(pc).x;
+#pragma unroll 8
+            for (int i = part; i < p.chunks; i += JOINERS / 32) {
+                const float2 v = __ldcg(pc + (size_t)i * s.groups);
+                const float n = (float)pixels_of(a, i) * (float)cg, d = v.x - first;
+                u = fmaf(n, d, u);
+                sq = fmaf(n * d, d, sq);
+                m2 += v.y;
+            }
+        }
+        sm[t] = make_float4(u, sq, m2, 0.f);
+        sync_joiners();
+        if (part == 0 && g < s.groups) {
+            for (int k = 1; k < JOINERS / 32; ++k) {
+                const float4 v = sm[k * 32 + t];
+                u += v.x;
+                sq += v.y;
+                m2 += v.z;
+            }
+            const float d = u / total, var = (m2 + (sq - u * d)) / total;
+            const float2 v = make_float2(first + d, rsqrtf((var < 0.f ? 0.f : var) + s.eps));
+            const size_t o = (size_t)set * s.groups + g;
+            a.sets[o] = v;
+            if (stats) {
+                stats[2 * o] = v.x;
+                stats[2 * o + 1] = v.y;
+            }
+        }
+        sync_joiners();
     }
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(NC_FWD + 32, 1)
+__global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     stream_forward_kernel(const Args a, const T* __restrict__ x, const T* __restrict__ gamma, const T* __restrict__ beta,
                           T* __restrict__ y, float* __restrict__ stats) {
     constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_FWD, WARPS = NC / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[2 * MAX_STAGES];
+    __shared__ uint64_t bars[2 * MAX_STAGES + 4];
+    __shared__ int unit_set[2];
     __shared__ Header headers[MAX_STAGES];
     __shared__ int flag;
-    const Ring ring = ring_of(smem, headers, bars, NC / 32);
+    __shared__ float4 scratch[JOINERS];
+    const Ring ring = ring_of(smem, headers, bars, unit_set, NC / 32);
+    if (threadIdx.x >= NC + 32) {
+        join_sets(a, ring, &flag, [&](int set) { join_stats(a, set, stats, scratch); });
+        return;
+    }
     if (threadIdx.x >= NC) {
         produce<T, 1>(a, ring, x, (const T*)nullptr, nullptr, true);
         return;
@@ -294,9 +374,14 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
     const int cg = s.C / s.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int tx = s.C / V, ty = NC / tx, cx = threadIdx.x % tx, ry = threadIdx.x / tx;
     const bool in = ry < ty;
+    // each channel's group (a division each, otherwise, for every unit)
+    uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
+    for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
+    sync_computing<NC>();
     // k: minus the unit's first pixel, or minus the mean; u, d: the sums, or rstd gamma and beta
     F2 k[P] = {}, u[P] = {}, d[P] = {};
     float* first = red + 2 * NC * V;  // [C] the unit's first pixel
+    Post post;
     volatile int none = 0;
     int stage = 0;
     uint32_t phase = 0;
@@ -304,9 +389,11 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
         if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
+        const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
+        const int n = min(p.srows, s.HW - hd.row0);
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
-        if (hd.pass == 0) {
-            if (hd.first) {
+        if (!apply) {
+            if (first_stage) {
                 unpack(k, q[0]);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
@@ -317,7 +404,7 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
             }
             if (in)
 #pragma unroll 4
-                for (int r = ry; r < hd.n; r += ty) {
+                for (int r = ry; r < n; r += ty) {
                     F2 v[P];
                     unpack(v, q[r * tx]);
 #pragma unroll
@@ -328,12 +415,12 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
                     }
                 }
         } else {
-            if (hd.first) {
+            if (first_stage) {
                 const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + p.data);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     const int c = (cx * P + i) * 2;
-                    const float2 v = st[c / cg], w = st[(c + 1) / cg];
+                    const float2 v = st[group[c]], w = st[group[c + 1]];
                     k[i] = f2(-v.x, -w.x);
                     u[i] = f2(v.y * (gamma ? ld1(gamma + c) : 1.f), w.y * (gamma ? ld1(gamma + c + 1) : 1.f));
                     d[i] = f2(beta ? ld1(beta + c) : 0.f, beta ? ld1(beta + c + 1) : 0.f);
@@ -342,7 +429,7 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
             if (in) {
                 T* yp = y + ((size_t)hd.set * s.HW + hd.row0) * s.C + cx * V;
 #pragma unroll 4
-                for (int r = ry; r < hd.n; r += ty) {
+                for (int r = ry; r < n; r += ty) {
                     F2 v[P];
                     unpack(v, q[r * tx]);
 #pragma unroll
@@ -354,10 +441,10 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
-        if (hd.pass == 0 && hd.last) {
+        if (!apply && last_stage) {
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
             sync_computing<NC>();
-            const float n = (float)(min((hd.chunk + 1) * p.rows, s.HW) - hd.chunk * p.rows);
+            const float count = (float)pixels_of(a, hd.chunk);
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
 #pragma unroll 8
@@ -365,7 +452,7 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
                     e += red[r * s.C + c];
                     f += red[(slots + r) * s.C + c];
                 }
-                const float m = e / n, m2 = f - e * m;  // about the first pixel
+                const float m = e / count, m2 = f - e * m;  // about the first pixel
                 red[c] = first[c] + m;
                 red[slots * s.C + c] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
             }
@@ -377,54 +464,84 @@ __global__ void __launch_bounds__(NC_FWD + 32, 1)
                 float m2 = 0.f;
                 for (int c = lane; c < cg; c += 32) {
                     const float f = red[g * cg + c] - mean;
-                    m2 += red[slots * s.C + g * cg + c] + n * f * f;
+                    m2 += red[slots * s.C + g * cg + c] + count * f * f;
                 }
                 m2 = warp_sum(m2);
                 if (lane == 0)
                     a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.groups + g] = make_float2(mean, m2);
             }
-            if (last_of_set<NC>(a, hd.set, &flag)) {
-                const float total = (float)s.HW * (float)cg;
-                auto count = [&](int i) { return (float)(min((i + 1) * p.rows, s.HW) - i * p.rows) * (float)cg; };
-                for (int g = warp; g < s.groups; g += WARPS) {
-                    const float2* pc = a.pieces + (size_t)hd.set * p.chunks * s.groups + g;
-                    float e = 0.f, m2 = 0.f;
-#pragma unroll 4
-                    for (int i = lane; i < p.chunks; i += 32) e += __ldcg(pc + (size_t)i * s.groups).x * (count(i) / total);
-                    const float mean = warp_sum(e);
-#pragma unroll 4
-                    for (int i = lane; i < p.chunks; i += 32) {
-                        const float2 v = __ldcg(pc + (size_t)i * s.groups);
-                        m2 += v.y + count(i) * (v.x - mean) * (v.x - mean);
-                    }
-                    m2 = warp_sum(m2);
-                    if (lane == 0) {
-                        const float2 v = make_float2(mean, rsqrtf(m2 / total + s.eps));
-                        const size_t o = (size_t)hd.set * s.groups + g;
-                        a.sets[o] = v;
-                        if (stats) {
-                            stats[2 * o] = v.x;
-                            stats[2 * o + 1] = v.y;
-                        }
-                    }
-                }
-                release_set<NC>(a, hd.set);
-            }
+            post(a, ring, hd.set);
+            sync_computing<NC>();  // red is free
         }
+    }
+    post(a, ring, -1);
+}
+
+// The backward's join: the sums of a set's channels, c1 and c2 of its groups; after the last set of all, the
+// parameters' gradients. sm: [2][MAX_C].
+template <typename T>
+__device__ __forceinline__ void join_sums(const Args& a, int set, const T* gamma, float* gg, float* gb, float* sm,
+                                          int* last) {
+    const NormShape& s = a.s;
+    const StreamPlan& p = a.p;
+    const int t = threadIdx.x - (blockDim.x - JOINERS), warp = t / 32, lane = t % 32, cg = s.C / s.groups;
+    float2* csums = a.sets;                    // [B][C] sums of a sample's channels
+    float2* c12 = a.sets + (size_t)s.B * s.C;  // [B][groups] (c1, c2)
+    for (int c = t; c < s.C; c += JOINERS) {
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll 16
+        for (int i = 0; i < p.chunks; ++i) {
+            const float2 w = __ldcg(a.pieces + ((size_t)set * p.chunks + i) * s.C + c);
+            v.x += w.x;
+            v.y += w.y;
+        }
+        csums[(size_t)set * s.C + c] = v;
+        const float k = gamma ? ld1(gamma + c) : 1.f;
+        sm[c] = k * v.x;
+        sm[MAX_C + c] = k * v.y;
+    }
+    sync_joiners();
+    const float inv = 1.f / ((float)s.HW * (float)cg);
+    for (int g = warp; g < s.groups; g += JOINERS / 32) {
+        float e = 0.f, f = 0.f;
+        for (int c = g * cg + lane; c < (g + 1) * cg; c += 32) {
+            e += sm[c];
+            f += sm[MAX_C + c];
+        }
+        e = warp_sum(e);
+        f = warp_sum(f);
+        if (lane == 0) c12[(size_t)set * s.groups + g] = make_float2(e * inv, f * inv);
+    }
+    if (gg || gb) {
+        sync_joiners();
+        if (t == 0) {
+            __threadfence();
+            *last = atomicAdd(a.finished, 1) == s.B - 1;
+            __threadfence();
+        }
+        sync_joiners();
+        if (*last)
+            for (int c = t; c < s.C; c += JOINERS) params_of(s, csums, c, gg, gb);
     }
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(NC_BWD + 32, 1)
+__global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     stream_backward_kernel(const Args a, const T* __restrict__ x, const T* __restrict__ gamma,
                            const T* __restrict__ beta, const float* __restrict__ stats, const T* __restrict__ gy,
                            T* __restrict__ gx, float* __restrict__ gg, float* __restrict__ gb) {
-    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_BWD, WARPS = NC / 32;
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_BWD;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t bars[2 * MAX_STAGES];
+    __shared__ uint64_t bars[2 * MAX_STAGES + 4];
+    __shared__ int unit_set[2];
     __shared__ Header headers[MAX_STAGES];
-    __shared__ int flag;
-    const Ring ring = ring_of(smem, headers, bars, NC / 32);
+    __shared__ int flag, last;
+    __shared__ float scratch[2 * MAX_C];
+    const Ring ring = ring_of(smem, headers, bars, unit_set, NC / 32);
+    if (threadIdx.x >= NC + 32) {
+        join_sets(a, ring, &flag, [&](int set) { join_sums(a, set, gamma, gg, gb, scratch, &last); });
+        return;
+    }
     if (threadIdx.x >= NC) {
         produce<T, 2>(a, ring, x, gy, stats, gx != nullptr);
         return;
@@ -432,11 +549,14 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     float* red = reinterpret_cast<float*>(smem + p.stages * p.stage);
-    const int cg = s.C / s.groups, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int cg = s.C / s.groups, lane = threadIdx.x % 32;
     const int tx = s.C / V, ty = NC / tx, cx = threadIdx.x % tx, ry = threadIdx.x / tx;
     const bool in = ry < ty;
-    float2* csums = a.sets;                    // [B][C] sums of a sample's channels
-    float2* c12 = a.sets + (size_t)s.B * s.C;  // [B][groups] (c1, c2)
+    // each channel's group (a division each, otherwise, for every unit)
+    uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
+    for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
+    sync_computing<NC>();
+    Post post;
     Channels<P> ch = {};
     F2 u[P] = {}, d[P] = {};  // the sums, or -c1 and -c2
 #pragma unroll
@@ -445,6 +565,7 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
         ch.ga[i] = f2(gamma ? ld1(gamma + c) : 1.f, gamma ? ld1(gamma + c + 1) : 1.f);
         ch.be[i] = f2(beta ? ld1(beta + c) : 0.f, beta ? ld1(beta + c + 1) : 0.f);
     }
+    ch.set_border();
     volatile int none = 0;
     int stage = 0;
     uint32_t phase = 0;
@@ -452,18 +573,20 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
         if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
+        const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
+        const int n = min(p.srows, s.HW - hd.row0);
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
         const uint4* h = reinterpret_cast<const uint4*>(smem + stage * p.stage + p.data) + cx;
-        if (hd.first) {
+        if (first_stage) {
             const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + 2 * p.data);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const int g0 = (cx * P + i) * 2 / cg, g1 = ((cx * P + i) * 2 + 1) / cg;
+                const int g0 = group[(cx * P + i) * 2], g1 = group[(cx * P + i) * 2 + 1];
                 const float2 v = st[g0], w = st[g1];
                 ch.nmean[i] = f2(-v.x, -w.x);
                 ch.rstd[i] = f2(v.y, w.y);
                 u[i] = d[i] = f2(0.f);
-                if (hd.pass == 1) {
+                if (apply) {
                     const float2 e = st[s.groups + g0], f = st[s.groups + g1];
                     u[i] = f2(-e.x, -f.x);
                     d[i] = f2(-e.y, -f.y);
@@ -471,9 +594,9 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
             }
         }
         if (in) {
-            if (hd.pass == 0) {
+            if (!apply) {
 #pragma unroll 2
-                for (int r = ry; r < hd.n; r += ty) {
+                for (int r = ry; r < n; r += ty) {
                     F2 v[P], g[P], dz[P], hat[P];
                     unpack(v, q[r * tx]);
                     unpack(g, h[r * tx]);
@@ -487,7 +610,7 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
             } else {
                 T* gp = gx + ((size_t)hd.set * s.HW + hd.row0) * s.C + cx * V;
 #pragma unroll 2
-                for (int r = ry; r < hd.n; r += ty) {
+                for (int r = ry; r < n; r += ty) {
                     F2 v[P], g[P], dz[P], hat[P];
                     unpack(v, q[r * tx]);
                     unpack(g, h[r * tx]);
@@ -501,7 +624,7 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
-        if (hd.pass == 0 && hd.last) {
+        if (!apply && last_stage) {
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
             sync_computing<NC>();
             for (int c = threadIdx.x; c < s.C; c += NC) {
@@ -513,51 +636,17 @@ __global__ void __launch_bounds__(NC_BWD + 32, 1)
                 }
                 a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.C + c] = make_float2(e, f);
             }
-            if (last_of_set<NC>(a, hd.set, &flag)) {
-                for (int c = threadIdx.x; c < s.C; c += NC) {
-                    float2 v = make_float2(0.f, 0.f);
-#pragma unroll 8
-                    for (int i = 0; i < p.chunks; ++i) {
-                        const float2 w = __ldcg(a.pieces + ((size_t)hd.set * p.chunks + i) * s.C + c);
-                        v.x += w.x;
-                        v.y += w.y;
-                    }
-                    csums[(size_t)hd.set * s.C + c] = v;
-                    const float k = gamma ? ld1(gamma + c) : 1.f;
-                    red[c] = k * v.x;
-                    red[s.C + c] = k * v.y;
-                }
-                sync_computing<NC>();
-                const float inv = 1.f / ((float)s.HW * (float)cg);
-                for (int g = warp; g < s.groups; g += WARPS) {
-                    float e = 0.f, f = 0.f;
-                    for (int c = g * cg + lane; c < (g + 1) * cg; c += 32) {
-                        e += red[c];
-                        f += red[s.C + c];
-                    }
-                    e = warp_sum(e);
-                    f = warp_sum(f);
-                    if (lane == 0) c12[(size_t)hd.set * s.groups + g] = make_float2(e * inv, f * inv);
-                }
-                release_set<NC>(a, hd.set);
-                if (gg || gb) {  // the last set of all sums the parameters' gradients
-                    if (threadIdx.x == 0) {
-                        flag = atomicAdd(a.finished, 1) == s.B - 1;
-                        __threadfence();
-                    }
-                    sync_computing<NC>();
-                    if (flag)
-                        for (int c = threadIdx.x; c < s.C; c += NC) params_of(s, csums, c, gg, gb);
-                }
-            }
+            post(a, ring, hd.set);
+            sync_computing<NC>();  // red is free
         }
     }
+    post(a, ring, -1);
 }
 
 template <typename F, typename... Q>
 cudaError_t launch(F f, DeviceFlags& flags, int threads, const Args& a, cudaStream_t st, Q... args) {
-    const uint32_t bytes = a.p.stages * a.p.stage + RED_BYTES + MAX_C * 4;
-    cudaError_t e = max_dynamic_smem_once((const void*)f, RING + RED_BYTES + MAX_C * 4, flags);
+    const uint32_t bytes = a.p.stages * a.p.stage + RED_BYTES + MAX_C * 6;
+    cudaError_t e = max_dynamic_smem_once((const void*)f, RING + RED_BYTES + MAX_C * 6, flags);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.p.grid);
@@ -592,7 +681,7 @@ template <typename T>
 cudaError_t forward_t(const Args& a, const T* x, const T* gamma, const T* beta, T* y, float* stats, cudaStream_t st) {
     return with_act(a.s.act, [&](auto A) {
         static DeviceFlags flags;
-        return launch(stream_forward_kernel<T, decltype(A)::value>, flags, NC_FWD + 32, a, st, x, gamma, beta, y, stats);
+        return launch(stream_forward_kernel<T, decltype(A)::value>, flags, NC_FWD + 32 + JOINERS, a, st, x, gamma, beta, y, stats);
     });
 }
 
@@ -601,7 +690,7 @@ cudaError_t backward_t(const Args& a, const T* x, const T* gamma, const T* beta,
                        float* gg, float* gb, cudaStream_t st) {
     return with_act(a.s.act, [&](auto A) {
         static DeviceFlags flags;
-        return launch(stream_backward_kernel<T, decltype(A)::value>, flags, NC_BWD + 32, a, st, x, gamma, beta, stats, gy, gx,
+        return launch(stream_backward_kernel<T, decltype(A)::value>, flags, NC_BWD + 32 + JOINERS, a, st, x, gamma, beta, stats, gy, gx,
                       gg, gb);
     });
 }

@@ -123,10 +123,20 @@ __device__ __forceinline__ float dz_of(float gy, float x, float hat, float mean,
     return act_grad<ACT, FAST>(gy, z);
 }
 
-// What the backward keeps of its channels (P pairs): -mean, rstd, gamma, beta.
+// What the backward keeps of its channels (P pairs): -mean, rstd, gamma, beta, and the largest near_border.
 template <int P>
 struct Channels {
     F2 nmean[P], rstd[P], ga[P], be[P];
+    float border;
+    __device__ __forceinline__ void set_border() {
+        border = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float a, b;
+            split(be[i], a, b);
+            border = fmaxf(border, fmaxf(near_border(a), near_border(b)));
+        }
+    }
     // dz and hat = (x - mean) rstd of a vector of x and of grad_y
     template <int ACT, bool FAST>
     __device__ __forceinline__ void dz(const F2 (&x)[P], const F2 (&gy)[P], F2 (&dz)[P], F2 (&hat)[P]) const {
@@ -140,17 +150,16 @@ struct Channels {
 #pragma unroll
             for (int i = 0; i < P; ++i) dz[i] = gy[i];
         } else if constexpr (ACT == kActRelu) {
-            bool near = false;
+            float least = 1e30f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                float z0, z1, g0, g1, b0, b1;
+                float z0, z1, g0, g1;
                 split(z[i], z0, z1);
                 split(gy[i], g0, g1);
-                split(be[i], b0, b1);
-                near |= fabsf(z0) < near_border(b0) || fabsf(z1) < near_border(b1);
+                least = fminf(least, fminf(fabsf(z0), fabsf(z1)));
                 dz[i] = f2(z0 > 0.f ? g0 : 0.f, z1 > 0.f ? g1 : 0.f);
             }
-            if (near)
+            if (least < border)
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     float x0, x1, g0, g1, m0, m1, r0, r1, a0, a1, b0, b1;
