@@ -751,7 +751,11 @@ size_t norm_workspace(const NormShape& s, int bf, bool backward) {
 
 cudaError_t norm_forward(const NormShape& s, int bf, bool vec, const void* x, const void* gamma, const void* beta,
                          void* y, float* stats, void* ws, unsigned* status, cudaStream_t st, int* launches) {
-    if (vec && norm_cluster_supported(s, bf, false)) {
+    // Clusters need one launch; a long queue, two with a ring, moves large maps faster: relu on 8x50x50x256 11.5 and
+    // 18.5 us, on 8x80x80x256 (26 MB) 27.7 and 25.0 us, on 64x28x28x512 48 and 35 us. (Backward the clusters lead
+    // wherever they fit: 64x28x28x512 82 and 118 us.)
+    const bool large = (double)s.B * s.HW * s.C * (bf ? 2 : 4) > 24e6 && norm_stream_supported(s, bf, false);
+    if (vec && !large && norm_cluster_supported(s, bf, false)) {
         ++*launches;
         return norm_cluster_forward(s, bf, x, gamma, beta, y, stats, st);
     }

@@ -21,7 +21,7 @@
 // are double buffered: the epilogue of a tile overlaps the next one's MMAs. The
 // epilogue adds bias and residual, applies the activation and stores whole
 // 32-byte sectors. Products with too few tiles to fill the GPU are split along
-// the reduction; the parts meet in reduce_kernel, in a fixed order.
+// the reduction; the parts meet in finish_kernel, in a fixed order.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -595,35 +595,68 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// ------------------------------------------------------------- the parts --
+// -------------------------------------------------- after the products --
 
-// D[m, n] = sum of the parts (in order), then the epilogue. Four columns a thread.
+// What remains after a product: a split reduction's parts to be joined, and grad_bias from the column sums of row
+// blocks. One kernel does both (either may be absent), so that neither waits for the other's launch.
 template <typename T>
-__global__ void __launch_bounds__(256) reduce_kernel(const float* __restrict__ part, int splits, long long stride, int M,
-                                                     int N, int pitch, const T* __restrict__ bias,
-                                                     const T* residual, T* y, T* z, int act) {
+struct FinishArgs {
+    // D[m, n] = sum of the parts (in order), then the epilogue; four columns a thread
+    const float* part;
+    long long stride;  // elements between two parts
+    int splits, M, N, pitch, part_blocks;
+    const T *bias, *residual;
+    T *y, *z;
+    int act;
+    // gb[n] = sum of sums[block][n]: 32 columns and eight lanes a block
+    const float* sums;
+    int sum_blocks, sum_pitch, sum_n, gb_blocks;
+    float* gb;
+};
+
+constexpr int FINISH_THREADS = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const FinishArgs<T> a) {
+    __shared__ float sm[FINISH_THREADS / 32][33];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n4 = (N + 3) / 4;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)M * n4; i += gridDim.x * 256LL) {
+    if ((int)blockIdx.x < a.gb_blocks) {
+        const int q = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + q;
+        float v = 0.f;
+        if (n < a.sum_n)
+#pragma unroll 16
+            for (int i = l; i < a.sum_blocks; i += FINISH_THREADS / 32) v += a.sums[(long long)i * a.sum_pitch + n];
+        sm[l][q] = v;
+        __syncthreads();
+        if (l == 0 && n < a.sum_n) {
+            for (int i = 1; i < FINISH_THREADS / 32; ++i) v += sm[i][q];
+            a.gb[n] = v;
+        }
+        return;
+    }
+    const int n4 = (a.N + 3) / 4;
+    const long long total = (long long)a.M * n4;
+    for (long long i = (blockIdx.x - a.gb_blocks) * (long long)FINISH_THREADS + threadIdx.x; i < total;
+         i += (long long)a.part_blocks * FINISH_THREADS) {
         const long long m = i / n4;
         const int n = (int)(i - m * n4) * 4;
-        const float* p = part + m * pitch + n;
+        const float* p = a.part + m * a.pitch + n;
         float v[4] = {};
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const float4 q = *reinterpret_cast<const float4*>(p + s * stride);
+#pragma unroll 10
+        for (int s = 0; s < a.splits; ++s) {
+            const float4 q = *reinterpret_cast<const float4*>(p + s * a.stride);
             v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (n + c < N) {
-                const long long at = m * N + n + c;
+            if (n + c < a.N) {
+                const long long at = m * a.N + n + c;
                 float s = v[c];
-                if (bias) s += ld1(bias + n + c);
-                if (residual) s += ld1(residual + at);
-                if (z) z[at] = from_float<T>(s);
-                y[at] = from_float<T>(act_run<kFast<T>>(s, act));
+                if (a.bias) s += ld1(a.bias + n + c);
+                if (a.residual) s += ld1(a.residual + at);
+                if (a.z) a.z[at] = from_float<T>(s);
+                a.y[at] = from_float<T>(act_run<kFast<T>>(s, a.act));
             }
     }
 }
@@ -717,89 +750,98 @@ __device__ __forceinline__ void store_terms(bf16* out, long long plane, const fl
 }
 
 // out[term][r][c] (bfloat16, rows of `pitch`) = the terms of in[r][c]; eight columns a thread.
-// VEC: rows of `in` are whole vectors, 16-byte aligned.
-template <typename T, int TERMS, bool VEC>
-__global__ void __launch_bounds__(256) pack_kernel(const T* __restrict__ in, int rows, int cols, int pitch,
-                                                   bf16* __restrict__ out) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c8 = pitch / 8;
-    const long long plane = (long long)rows * pitch;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)rows * c8; i += gridDim.x * 256LL) {
+// vec: rows of `in` are whole vectors, 16-byte aligned.
+template <typename T>
+struct PackJob {
+    const T* in;
+    int rows, cols, pitch, vec, blocks;
+    bf16* out;
+};
+// dz = grad_y act'(saved): its bfloat16 terms (out, as PackJob; may be null), grad_residual (may be null), and the
+// column sums of a block's rows (sums[row block][pitch]; may be null). A thread keeps eight columns and walks the
+// block's rows. vec as for PackJob, for gy, saved and gr.
+template <typename T>
+struct DzJob {
+    const T *gy, *saved;
+    int M, N, pitch, rows, cblocks, vec, blocks;
+    bf16* out;
+    T* gr;
+    float* sums;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void run_pack(const PackJob<T>& j, int block) {
+    constexpr int TERMS = std::is_same<T, bf16>::value ? 1 : 3;
+    const int c8 = j.pitch / 8;
+    const long long plane = (long long)j.rows * j.pitch;
+    for (long long i = block * 256LL + threadIdx.x; i < (long long)j.rows * c8; i += j.blocks * 256LL) {
         const long long r = i / c8;
         const int c = (int)(i - r * c8) * 8;
         float v[8];
-        load8<VEC>(v, in + r * cols + c, cols - c);
-        store_terms<TERMS>(out + r * pitch + c, plane, v);
+        load8<VEC>(v, j.in + r * j.cols + c, j.cols - c);
+        store_terms<TERMS>(j.out + r * j.pitch + c, plane, v);
     }
 }
 
-// dz = grad_y act'(saved): its bfloat16 terms (out, as pack_kernel; may be null), grad_residual (may be null), and
-// the column sums of a block's rows (sums[block][pitch]; may be null). A thread keeps eight columns and walks the
-// block's rows. VEC as for pack_kernel, for gy, saved and gr.
 template <typename T, int ACT, int TERMS, bool VEC>
-__global__ void __launch_bounds__(256) dz_kernel(const T* __restrict__ gy, const T* __restrict__ saved, int M, int N,
-                                                 int pitch, int rows, int cblocks, bf16* __restrict__ out,
-                                                 T* __restrict__ gr, float* __restrict__ sums) {
-    __shared__ float sm[256 * 8];
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c8 = pitch / 8;
+__device__ __forceinline__ void run_dz(const DzJob<T>& j, int block, float* sm) {
+    const int c8 = j.pitch / 8;
     const int tx = min(c8, 256), ty = 256 / tx;
     const int cx = threadIdx.x % tx, ry = threadIdx.x / tx;
-    const int rb = blockIdx.x / cblocks;
-    const int c = ((blockIdx.x % cblocks) * tx + cx) * 8;
-    const long long plane = (long long)M * pitch;
-    const int m0 = rb * rows, m1 = min(m0 + rows, M);
+    const int rb = block / j.cblocks;
+    const int c = ((block % j.cblocks) * tx + cx) * 8;
+    const long long plane = (long long)j.M * j.pitch;
+    const int m0 = rb * j.rows, m1 = min(m0 + j.rows, j.M);
     float sum[8] = {};
-    if (c < pitch && ry < ty) {
+    if (c < j.pitch && ry < ty) {
 #pragma unroll 4
         for (long long m = m0 + ry; m < m1; m += ty) {
-            const long long at = m * N + c;
+            const long long at = m * j.N + c;
             float v[8];
-            load8<VEC>(v, gy + at, N - c);
+            load8<VEC>(v, j.gy + at, j.N - c);
             if constexpr (ACT != kActNone) {
                 float s[8];
-                load8<VEC>(s, saved + at, N - c);
+                load8<VEC>(s, j.saved + at, j.N - c);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = act_grad<ACT, kFast<T>>(v[q], s[q]);
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q) sum[q] += v[q];
-            if (gr) store8<VEC>(gr + at, v, N - c);
-            if (out) store_terms<TERMS>(out + m * pitch + c, plane, v);
+            if (j.gr) store8<VEC>(j.gr + at, v, j.N - c);
+            if (j.out) store_terms<TERMS>(j.out + m * j.pitch + c, plane, v);
         }
     }
-    if (!sums) return;
+    if (!j.sums) return;
 #pragma unroll
     for (int q = 0; q < 8; ++q) sm[threadIdx.x * 8 + q] = sum[q];
     __syncthreads();
-    if (ry == 0 && c < pitch) {
+    if (ry == 0 && c < j.pitch) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             float v = 0.f;
             for (int r = 0; r < ty; ++r) v += sm[(r * tx + cx) * 8 + q];
-            sums[(long long)rb * pitch + c + q] = v;
+            j.sums[(long long)rb * j.pitch + c + q] = v;
         }
     }
 }
 
-// grad_bias[n] = sum over the row blocks (32 columns, 8 lanes a block)
-__global__ void __launch_bounds__(256) bias_kernel(const float* __restrict__ sums, int blocks, int pitch, int N,
-                                                   float* __restrict__ gb) {
-    __shared__ float sm[8][33];
+// All of a call's operand preparation in one launch.
+template <typename T, int ACT, int TERMS>
+__global__ void __launch_bounds__(256) prep_kernel(const DzJob<T> dz, const PackJob<T> a, const PackJob<T> b) {
+    __shared__ float sm[256 * 8];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int q = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + q;
-    float v = 0.f;
-    if (n < N)
-        for (int i = l; i < blocks; i += 8) v += sums[(long long)i * pitch + n];
-    sm[l][q] = v;
-    __syncthreads();
-    if (l == 0 && n < N) {
-        for (int i = 1; i < 8; ++i) v += sm[i][q];
-        gb[n] = v;
+    int block = blockIdx.x;
+    if (block < dz.blocks) {
+        if (dz.vec) run_dz<T, ACT, TERMS, true>(dz, block, sm);
+        else run_dz<T, ACT, TERMS, false>(dz, block, sm);
+        return;
     }
+    block -= dz.blocks;
+    const PackJob<T>& j = block < a.blocks ? a : b;
+    if (block >= a.blocks) block -= a.blocks;
+    if (j.vec) run_pack<T, true>(j, block);
+    else run_pack<T, false>(j, block);
 }
 
 // ------------------------------------------------------------------- host --
@@ -945,12 +987,34 @@ size_t part_bytes(const GemmPlan& p, long long rows, long long cols) {
     return p.splits > 1 ? (size_t)p.splits * rows * ((cols + 7) / 8 * 8) * 4 : 0;
 }
 
-// D [rows, cols] (rows of `cols`) = A B^T through the epilogue. A: K-major [rows, red], or (a_mn) [red, rows]; B alike
+// grad_bias from the column sums of row blocks (gb null: not asked for).
+struct Sums {
+    const float* sums;
+    int blocks, pitch, n;
+    float* gb;
+};
+template <typename T>
+void bias_job(FinishArgs<T>& f, const Sums& s) {
+    if (!s.gb) return;
+    f.sums = s.sums;
+    f.sum_blocks = s.blocks;
+    f.sum_pitch = s.pitch;
+    f.sum_n = s.n;
+    f.gb = s.gb;
+    f.gb_blocks = (s.n + 31) / 32;
+}
+template <typename T>
+cudaError_t finish(const FinishArgs<T>& f, cudaStream_t st, int* launches) {
+    ++*launches;
+    return launch(finish_kernel<T>, f.gb_blocks + f.part_blocks, FINISH_THREADS, 0, 1, st, f);
+}
+
+// D [rows, cols] (rows of `cols`) = A B^T through the epilogue, and (sums) grad_bias after it. A: K-major [rows, red], or (a_mn) [red, rows]; B alike
 // with cols. `parts`: room for the split reduction's results.
 template <typename T>
 cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix& B, bool b_mn, int rows, int cols,
-                     int red, const Out<T>& out, float* parts, bool f32_out, unsigned* status, cudaStream_t st,
-                     int* launches) {
+                     int red, const Out<T>& out, float* parts, bool f32_out, const Sums& sums, unsigned* status,
+                     cudaStream_t st, int* launches) {
     const Matrix &L = p.swap ? B : A, &R = p.swap ? A : B;
     const bool l_mn = p.swap ? b_mn : a_mn, r_mn = p.swap ? a_mn : b_mn;
     GemmArgs a = {};
@@ -1028,11 +1092,27 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     if (e != cudaSuccess) return e;
     ++*launches;
     if (split) {
-        const long long n = ((long long)rows * ((cols + 3) / 4) + 255) / 256;
-        e = launch(reduce_kernel<T>, (int)std::min<long long>(n, num_sms() * 8), 256, 0, 1, st, (const float*)parts,
-                   p.splits, a.part, rows, cols, pitch, out.bias, out.residual, out.y, out.z, out.act);
-        if (e != cudaSuccess) return e;
-        ++*launches;
+        FinishArgs<T> f = {};
+        f.part = parts;
+        f.stride = a.part;
+        f.splits = p.splits;
+        f.M = rows;
+        f.N = cols;
+        f.pitch = pitch;
+        f.part_blocks = (int)std::min<long long>(((long long)rows * ((cols + 3) / 4) + FINISH_THREADS - 1) / FINISH_THREADS,
+                                                 num_sms() * 8);
+        f.bias = out.bias;
+        f.residual = out.residual;
+        f.y = out.y;
+        f.z = out.z;
+        f.act = out.act;
+        bias_job(f, sums);
+        return finish(f, st, launches);
+    }
+    if (sums.gb) {
+        FinishArgs<T> f = {};
+        bias_job(f, sums);
+        return finish(f, st, launches);
     }
     return cudaSuccess;
 }
@@ -1087,7 +1167,7 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
     p.tx = std::min(c8, 256);
     p.ty = 256 / p.tx;
     p.cblocks = (c8 + p.tx - 1) / p.tx;
-    long long want = std::max(1, num_sms() * 4 / p.cblocks);
+    long long want = std::max(1, num_sms() * 2 / p.cblocks);
     want = std::min<long long>(want, (s.M + 4LL * p.ty - 1) / (4LL * p.ty));
     p.rows = (int)((s.M + want - 1) / want);
     p.rblocks = (s.M + p.rows - 1) / p.rows;
@@ -1106,14 +1186,25 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
 }
 
 template <typename T>
-cudaError_t pack(const T* in, int rows, int cols, void* out, cudaStream_t st, int* launches) {
+PackJob<T> pack_job(const T* in, int rows, int cols, void* out) {
     const int pitch = up8(cols);
     const long long n = ((long long)rows * (pitch / 8) + 255) / 256;
+    return {in, rows, cols, pitch, cols % 8 == 0 && ((uintptr_t)in & 15) == 0,
+            (int)std::min<long long>(n, num_sms() * 16), (bf16*)out};
+}
+
+template <typename T>
+cudaError_t prepare(int act, const DzJob<T>& dz, const PackJob<T>& a, const PackJob<T>& b, cudaStream_t st,
+                    int* launches) {
+    const int blocks = dz.blocks + a.blocks + b.blocks;
+    if (!blocks) return cudaSuccess;
     ++*launches;
-    constexpr int TERMS = std::is_same<T, bf16>::value ? 1 : 3;
-    const bool vec = cols % 8 == 0 && ((uintptr_t)in & 15) == 0;
-    return launch(vec ? pack_kernel<T, TERMS, true> : pack_kernel<T, TERMS, false>,
-                  (int)std::min<long long>(n, num_sms() * 16), 256, 0, 1, st, in, rows, cols, pitch, (bf16*)out);
+    return with_act(dz.blocks ? act : kActNone, [&](auto A) {
+        constexpr int ACT = decltype(A)::value;
+        // as BwdPlan::dz_terms
+        constexpr int TERMS = std::is_same<T, bf16>::value && (ACT == kActNone || ACT == kActRelu) ? 1 : 3;
+        return launch(prep_kernel<T, ACT, TERMS>, blocks, 256, 0, 1, st, dz, a, b);
+    });
 }
 
 template <typename T>
@@ -1123,17 +1214,19 @@ cudaError_t forward_t(const LinearShape& s, const T* x, const T* w, const T* bia
     const FwdPlan p = plan_forward(s, bf);
     const int terms = bf ? 1 : 3;
     Matrix X{x, s.M, s.K, s.K, 1}, W{w, s.N, s.K, s.K, 1};
-    cudaError_t e;
+    PackJob<T> jx = {}, jw = {};
     if (p.pack_x) {
-        if ((e = pack(x, s.M, s.K, ws + p.x, st, launches)) != cudaSuccess) return e;
+        jx = pack_job(x, s.M, s.K, ws + p.x);
         X = {ws + p.x, s.M, s.K, up8(s.K), terms};
     }
     if (p.pack_w) {
-        if ((e = pack(w, s.N, s.K, ws + p.w, st, launches)) != cudaSuccess) return e;
+        jw = pack_job(w, s.N, s.K, ws + p.w);
         W = {ws + p.w, s.N, s.K, up8(s.K), terms};
     }
+    const cudaError_t e = prepare<T>(kActNone, DzJob<T>{}, jx, jw, st, launches);
+    if (e != cudaSuccess) return e;
     return run_gemm<T>(p.g, X, false, W, false, s.M, s.N, s.K, Out<T>{bias, residual, y, z, s.act},
-                       (float*)(ws + p.parts), !bf, status, st, launches);
+                       (float*)(ws + p.parts), !bf, Sums{}, status, st, launches);
 }
 
 template <typename T>
@@ -1142,49 +1235,42 @@ cudaError_t backward_t(const LinearShape& s, const T* x, const T* w, const T* sa
     constexpr int bf = std::is_same<T, bf16>::value;
     const BwdPlan p = plan_backward(s, bf);
     const int terms = bf ? 1 : 3;
-    cudaError_t e;
     Matrix X{x, s.M, s.K, s.K, 1}, W{w, s.N, s.K, s.K, 1}, DZ{gy, s.M, s.N, s.N, 1};
-    const bool need_dz = gx || gw;
-    bf16* dz = p.pass_dz && need_dz ? (bf16*)(ws + p.dz) : nullptr;
+    bf16* dz = p.pass_dz && (gx || gw) ? (bf16*)(ws + p.dz) : nullptr;
+    DzJob<T> jd = {};
+    PackJob<T> jx = {}, jw = {};
     if (dz || gb || gr) {
-        const bool vec = s.N % 8 == 0 && (((uintptr_t)gy | (uintptr_t)saved | (uintptr_t)gr) & 15) == 0;
-        e = with_act(s.act, [&](auto A) {
-            constexpr int ACT = decltype(A)::value;
-            // as BwdPlan::dz_terms
-            constexpr int TERMS = bf && (ACT == kActNone || ACT == kActRelu) ? 1 : 3;
-            return launch(vec ? dz_kernel<T, ACT, TERMS, true> : dz_kernel<T, ACT, TERMS, false>, p.rblocks * p.cblocks,
-                          256, 0, 1, st, gy, saved, s.M, s.N, up8(s.N), p.rows, p.cblocks, dz, gr,
-                          gb ? (float*)(ws + p.sums) : (float*)nullptr);
-        });
-        if (e != cudaSuccess) return e;
-        ++*launches;
+        jd = {gy,  saved, s.M, s.N, up8(s.N), p.rows, p.cblocks,
+              s.N % 8 == 0 && (((uintptr_t)gy | (uintptr_t)saved | (uintptr_t)gr) & 15) == 0,
+              p.rblocks * p.cblocks, dz, gr, gb ? (float*)(ws + p.sums) : nullptr};
         if (dz) DZ = {dz, s.M, s.N, up8(s.N), p.dz_terms};
     }
-    if (gb) {
-        e = launch(bias_kernel, (s.N + 31) / 32, 256, 0, 1, st, (const float*)(ws + p.sums), p.rblocks, up8(s.N), s.N,
-                   gb);
-        if (e != cudaSuccess) return e;
-        ++*launches;
+    if (gx && p.pack_w) {
+        jw = pack_job(w, s.N, s.K, ws + p.w);
+        W = {ws + p.w, s.N, s.K, up8(s.K), terms};
     }
+    if (gw && p.pack_x) {
+        jx = pack_job(x, s.M, s.K, ws + p.x);
+        X = {ws + p.x, s.M, s.K, up8(s.K), terms};
+    }
+    cudaError_t e = prepare<T>(s.act, jd, jx, jw, st, launches);
+    if (e != cudaSuccess) return e;
+    const Sums sums{(const float*)(ws + p.sums), p.rblocks, up8(s.N), s.N, gb};
     if (gx) {
-        if (p.pack_w) {
-            if ((e = pack(w, s.N, s.K, ws + p.w, st, launches)) != cudaSuccess) return e;
-            W = {ws + p.w, s.N, s.K, up8(s.K), terms};
-        }
         Matrix first = DZ;
         first.terms = terms;
         e = run_gemm<T>(p.gx, first, false, W, true, s.M, s.K, s.N, Out<T>{nullptr, nullptr, gx, nullptr, kActNone},
-                        (float*)(ws + p.parts), !bf, status, st, launches);
+                        (float*)(ws + p.parts), !bf, gw ? Sums{} : sums, status, st, launches);
         if (e != cudaSuccess) return e;
     }
-    if (gw) {
-        if (p.pack_x) {
-            if ((e = pack(x, s.M, s.K, ws + p.x, st, launches)) != cudaSuccess) return e;
-            X = {ws + p.x, s.M, s.K, up8(s.K), terms};
-        }
-        e = run_gemm<float>(p.gw, DZ, true, X, true, s.N, s.K, s.M, Out<float>{nullptr, nullptr, gw, nullptr, kActNone},
-                            (float*)(ws + p.parts), true, status, st, launches);
-        if (e != cudaSuccess) return e;
+    if (gw)
+        return run_gemm<float>(p.gw, DZ, true, X, true, s.N, s.K, s.M,
+                               Out<float>{nullptr, nullptr, gw, nullptr, kActNone}, (float*)(ws + p.parts), true, sums,
+                               status, st, launches);
+    if (gb && !gx) {
+        FinishArgs<T> f = {};
+        bias_job(f, sums);
+        return finish(f, st, launches);
     }
     return cudaSuccess;
 }
