@@ -58,6 +58,7 @@ struct Operand {
 struct GemmArgs {
     int rows, cols;        // D: A-side rows, B-side rows
     int kblocks, splits;   // stages of 64; parts along the reduction
+    int kper, kmore;       // stages a part, and parts with one more
     int chunk;             // stages between two reads of the accumulator
     int mt, nt;            // tiles
     int bn;                // B rows a tile (of the CTA or pair)
@@ -318,13 +319,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int units = a.mt * a.nt * a.splits;
+    // (32-bit divisions, and none where there is nothing to divide: 20000x1024x256 took 17.2 us with 64-bit ones, 14.4 so)
     auto unit_of = [&](int u, int& im, int& in, int& k0, int& k1, int& sp) {
-        sp = u % a.splits;
-        const int t = u / a.splits;
-        in = t % a.nt;
-        im = t / a.nt;
-        k0 = (int)((long long)a.kblocks * sp / a.splits);
-        k1 = (int)((long long)a.kblocks * (sp + 1) / a.splits);
+        int t = u;
+        sp = 0;
+        k0 = 0;
+        k1 = a.kblocks;
+        if (a.splits > 1) {
+            t = (int)((unsigned)u / (unsigned)a.splits);
+            sp = u - t * a.splits;
+            k0 = sp * a.kper + min(sp, a.kmore);
+            k1 = k0 + a.kper + (sp < a.kmore);
+        }
+        im = t;
+        in = 0;
+        if (a.nt > 1) {
+            im = (int)((unsigned)t / (unsigned)a.nt);
+            in = t - im * a.nt;
+        }
     };
 
     if (warp == 0 || warp == B_WARP) {
@@ -736,6 +748,26 @@ __device__ __forceinline__ void store_terms(bf16* out, long long plane, const fl
     if constexpr (TERMS == 1) {
         *reinterpret_cast<uint4*>(out) = pack8(v);
     } else {
+        float most = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) most = fmaxf(most, fabsf(v[q]));
+        if (most < 3.38e38f) {  // none infinite, nor rounded to infinity (a NaN may stay one in every term)
+            float r[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) r[q] = v[q];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const uint4 t = pack8(r);
+                *reinterpret_cast<uint4*>(out + k * plane) = t;
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    r[2 * q] -= __uint_as_float(w[q] << 16);
+                    r[2 * q + 1] -= __uint_as_float(w[q] & 0xFFFF0000u);
+                }
+            }
+            return;
+        }
         bf16 t[3][8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -923,11 +955,14 @@ struct GemmPlan {
 
 // The cheapest of the tilings by a model of one CTA's cycles: per stage the larger of the MMAs (128 x 64 x bn at
 // 4096 a cycle, for each product of terms) and the operands' bytes from L2 (56 a cycle measured), per tile the
-// result's bytes (24 a cycle, an SM's share of HBM), and the parts' way through L2 where the reduction is split.
-GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool f32_out, int out_bytes) {
+// result's bytes (24 a cycle, an SM's share of HBM) with the activation's cost and 700 cycles of its own, and the
+// parts' way through L2 and a second launch where the reduction is split (grad_weight of 20000x256x1024: 18 parts of
+// 256 x 256 tiles 24.8 us, nine of 256 x 128 22.8 us).
+GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool f32_out, int out_bytes, int act) {
     const int kblocks = (red + BK - 1) / BK;
     const int sms = num_sms();
     const int prods = ta == 1 ? 1 : tb == 1 ? 3 : 6;
+    const double element = out_bytes / 24.0 + (act == kActSilu || act == kActGelu ? 0.2 : 0.0);
     GemmPlan best = {};
     double best_t = 1e300;
     for (int swap = 0; swap < 2; ++swap) {
@@ -942,20 +977,18 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
                 const long long mt = (r + BM * cg - 1) / (BM * cg), nt = (c + bn - 1) / bn;
                 const int slots = sms / cg;
                 const double stage = std::max(2.0 * bn * prods, (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
-                const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * out_bytes / 24.0;
+                const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * element, part = BM * bn * 4 / 20.0;
                 // no split, or as many parts as fill the GPU once, or half of them
                 const int fill = (int)std::min<long long>(kblocks, std::max<long long>(1, slots / (mt * nt)));
                 int last = 0;
                 for (const int splits : {1, fill / 2, fill}) {
                     if (splits <= last) continue;
                     last = splits;
-                    const long long units = mt * nt * splits;
-                    const long long waves = (units + slots - 1) / slots;
+                    const long long waves = (mt * nt * splits + slots - 1) / slots;
                     const int kb = (kblocks + splits - 1) / splits;
-                    double t = waves * std::max(kb * stage, splits > 1 ? BM * bn * 4 / 40.0 : epi) +
-                               (splits > 1 ? BM * bn * 4 / 40.0 : epi) + 2000.0;
-                    if (splits > 1)
-                        t += 2500.0 + (double)rows * cols * (4.0 * splits + out_bytes) / (sms * 40.0);
+                    double t = waves * (std::max(kb * stage, splits > 1 ? part : epi) + 700.0) +
+                               (splits > 1 ? part : epi) + 2000.0;
+                    if (splits > 1) t += 4000.0 + (double)rows * cols * (4.0 * splits + out_bytes) / (sms * 12.0);
                     if (t < best_t) {
                         best_t = t;
                         best = {swap != 0, cg, bn, splits, 0};
@@ -1022,6 +1055,8 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.cols = p.swap ? rows : cols;
     a.kblocks = (red + BK - 1) / BK;
     a.splits = p.splits;
+    a.kper = a.kblocks / p.splits;
+    a.kmore = a.kblocks % p.splits;
     a.chunk = p.chunk;
     a.mt = (a.rows + BM * p.cg - 1) / (BM * p.cg);
     a.nt = (a.cols + p.bn - 1) / p.bn;
@@ -1132,7 +1167,7 @@ FwdPlan plan_forward(const LinearShape& s, int bf) {
     bool xw, gy;
     linear_tc_in_place(s, bf, &xw, &gy);
     p.pack_x = p.pack_w = !xw;
-    p.g = plan_gemm(s.M, s.N, s.K, terms, terms, !bf, bf ? 2 : 4);
+    p.g = plan_gemm(s.M, s.N, s.K, terms, terms, !bf, bf ? 2 : 4, s.act);
     size_t o = 0;
     p.x = o;
     if (p.pack_x) o = up256(o + (size_t)terms * s.M * up8(s.K) * 2);
@@ -1161,13 +1196,13 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
     // others
     p.dz_terms = bf && !smooth ? 1 : 3;
     // grad_x of a bfloat16 layer reads the first term alone: dz rounded once, as a grad_x in bfloat16 is
-    p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4);
-    p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4);
+    p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4, kActNone);
+    p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4, kActNone);
     const int c8 = up8(s.N) / 8;
     p.tx = std::min(c8, 256);
     p.ty = 256 / p.tx;
     p.cblocks = (c8 + p.tx - 1) / p.tx;
-    long long want = std::max(1, num_sms() * 2 / p.cblocks);
+    long long want = std::max(1, num_sms() * 4 / p.cblocks);
     want = std::min<long long>(want, (s.M + 4LL * p.ty - 1) / (4LL * p.ty));
     p.rows = (int)((s.M + want - 1) / want);
     p.rblocks = (s.M + p.rows - 1) / p.rows;
