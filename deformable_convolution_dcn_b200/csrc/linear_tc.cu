@@ -953,8 +953,8 @@ struct GemmPlan {
     int cg, bn, splits, chunk;
 };
 
-// The cheapest of the tilings by a model of one CTA's cycles: per stage the larger of the MMAs (128 x 64 x bn at
-// 4096 a cycle, for each product of terms) and the operands' bytes from L2 (56 a cycle measured), per tile the
+// The cheapest of the tilings by a model of one CTA's cycles: per stage the larger of the MMAs (bn / 2
+// cycles each, but 75 to issue one, and 150 to wait and commit) and the operands' bytes from L2 (56 a cycle), per tile the
 // result's bytes (24 a cycle, an SM's share of HBM) with the activation's cost and 700 cycles of its own, and the
 // parts' way through L2 and a second launch where the reduction is split (grad_weight of 20000x256x1024: 18 parts of
 // 256 x 256 tiles 24.8 us, nine of 256 x 128 22.8 us).
@@ -976,8 +976,9 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
                 if (prods == 6 && cg == 1 && bn == 128) continue;  // shared memory holds one stage only
                 const long long mt = (r + BM * cg - 1) / (BM * cg), nt = (c + bn - 1) / bn;
                 const int slots = sms / cg;
-                const double stage = std::max(2.0 * bn * prods, (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
-                const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * element, part = BM * bn * 4 / 20.0;
+                const double stage = std::max(4.0 * prods * std::max(bn / 2.0, 75.0) + 150.0,
+                                              (sa * (double)A_BYTES + sb * bn / cg * 128.0) / 56.0);
+                const double epi = BM * (double)bn * (swap ? 2.0 : 1.0) * element, part = BM * bn * (swap ? 3.0 : 1.0) * 4 / 20.0;
                 // no split, or as many parts as fill the GPU once, or half of them
                 const int fill = (int)std::min<long long>(kblocks, std::max<long long>(1, slots / (mt * nt)));
                 int last = 0;

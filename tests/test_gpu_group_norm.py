@@ -15,7 +15,11 @@ EPS = 1e-5
 SIZES = [(1, 1, 1, 1, 1), (2, 1, 1, 64, 8), (3, 5, 7, 30, 3), (1, 7, 10, 256, 32), (2, 9, 13, 66, 6), (2, 8, 8, 24, 2),
          (1, 6, 5, 40, 40), (2, 11, 3, 12, 1), (1, 50, 50, 256, 32), (2, 100, 90, 64, 16), (5, 4, 4, 2048, 32),
          (1, 3, 3, 4104, 2), (1, 2, 5, 2049, 1), (1, 130, 257, 8, 1), (70, 3, 2, 16, 4), (2, 33, 31, 96, 32),
-         (1, 200, 210, 128, 32), (2, 40, 40, 520, 40), (1, 64, 64, 1088, 64)]
+         (1, 200, 210, 128, 32), (2, 40, 40, 520, 40), (1, 64, 64, 1088, 64),
+         # long maps by the queue with a ring: many samples, uneven runs, a group a channel, one group, wide rows
+         (3, 129, 131, 96, 32), (9, 90, 101, 64, 64), (2, 150, 140, 72, 1), (1, 257, 129, 1024, 32), (160, 33, 31, 64, 8),
+         # the same without whole vectors, and blocks of groups wider than a unit
+         (3, 129, 131, 33, 3), (2, 61, 67, 1536, 2), (1, 300, 301, 3, 1)]
 
 
 def make(B, H, W, C, dtype, affine=True, level=0.7, seed=0):

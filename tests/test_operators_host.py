@@ -142,3 +142,24 @@ def test_binding_rejects_shapes():
         dcn.group_norm_forward(x, None, None, 2)
     with pytest.raises(ValueError, match="activation"):
         dcn.group_norm_forward(m, None, None, 2, activation="elu")
+
+
+def test_workspace_sizes(lib):
+    # the tensor-core kernels of a layer without rows or kept off them need none
+    assert dcn.linear_workspace_size(LP(M=0), dcn.OP_FORWARD) == 0
+    assert dcn.linear_workspace_size(LP(flags=dcn.DCN_FLAG_GENERIC), dcn.OP_BACKWARD) == 0
+    # bfloat16 rows of whole vectors are read in place; others are copied, float32 in three terms
+    assert dcn.linear_workspace_size(LP(M=4096, N=256, K=64), dcn.OP_FORWARD) == 0
+    assert dcn.linear_workspace_size(LP(M=4096, N=256, K=65), dcn.OP_FORWARD) >= 2 * (4096 + 256) * 72
+    assert dcn.linear_workspace_size(LP(M=4096, N=256, K=64, dtype=0), dcn.OP_FORWARD) >= 6 * (4096 + 256) * 64
+    n = dcn.linear_workspace_size(LP(M=4096, N=256, K=65), dcn.OP_FORWARD)
+    p = LP(M=4096, N=256, K=65)
+    assert lin_fwd(lib, p, ws=None) == EWS
+    assert lin_fwd(lib, p, n=n - 1) == EWS
+    assert str(n) in lib.dcn_last_error_string().decode()
+    assert lin_fwd(lib, p, ws=ctypes.c_void_p((1 << 20) + 128)) == EUNSUP
+    n = dcn.linear_workspace_size(p, dcn.OP_BACKWARD)
+    assert n > 0 and lin_bwd(lib, p, n=n - 1) == EWS
+    # sizes do not depend on where they are asked for, nor grow past what the tensors justify
+    assert dcn.linear_workspace_size(LP(M=8, N=1024, K=12544), dcn.OP_FORWARD) <= 64 * 8 * 1024 * 4
+    assert dcn.group_norm_workspace_size(NP(B=8, H=200, W=200, C=128, groups=32), dcn.OP_FORWARD) < 1 << 22
