@@ -21,7 +21,6 @@ parameter gradients are float32.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -53,6 +52,7 @@ DCN_FLAG_GENERIC = 0x1
 DCN_FLAG_NO_TF32 = 0x2
 DCN_ERR_TIMEOUT, DCN_ERR_RANGE = -4, -6
 OP_FORWARD, OP_BACKWARD_DATA, OP_BACKWARD_WEIGHT, OP_BACKWARD = 0, 1, 2, 3
+OP_ALIGNED = 0x100
 _MOST = 2 ** 31 - 1  # elements of a tensor that the library indexes
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 _DTYPES = {torch.float32: DCN_F32, torch.bfloat16: DCN_BF16}
@@ -352,14 +352,16 @@ def _check_shape(name, t, shape):
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _check_like(like, shapes, /, **ts):
-    """Each tensor that is not None is contiguous, of the device and dtype of `like`, and of its shape in `shapes`."""
-    dtype, device = like.dtype, like.device
-    for name, t in ts.items():
-        if t is not None and (t.dtype is not dtype or t.device != device or not t.is_contiguous()
-                              or t.shape != shapes[name]):
-            _check_tensors(dtype, device, **{name: t})
-            _check_shape(name, t, shapes[name])
+def _fits(t, dtype, device, shape):
+    return t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
+
+
+def _refuse(dtype, device, **ts):
+    """Raises for the first of name=(tensor or None, shape) that is not contiguous, on `device` and of `dtype` and
+    `shape`."""
+    for name, (t, shape) in ts.items():
+        _check_tensors(dtype, device, **{name: t})
+        _check_shape(name, t, shape)
 
 
 def _addr(t):
@@ -378,19 +380,32 @@ def _scratch(n, x, workspace):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(fn, x, *args):
-    """fn(*args, stream) on x's device and its current stream."""
-    index = x.device.index
+def _call(fn, index, *args):
+    """fn(*args, stream) on device `index` and its current stream."""
     if index == torch._C._cuda_getDevice():
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc)
 
 
-def _on_device(x):
-    """The context in which sizes that depend on the device are asked for: x's device."""
-    return contextlib.nullcontext() if x.device.index == torch._C._cuda_getDevice() else torch.cuda.device(x.device)
+def _sizes_on(index, sizes, *fields):
+    """sizes(index, *fields) with device `index` current."""
+    if index == torch._C._cuda_getDevice():
+        return sizes(index, *fields)
+    with torch.cuda.device(index):
+        return sizes(index, *fields)
+
+
+def _map_device(x):
+    """x's device number; refuses what the library cannot index."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor, got %s" % x.device)
+    if x.numel() > _MOST:
+        raise ValueError("a tensor exceeds 2^31-1 elements")
+    return x.get_device()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -401,26 +416,26 @@ def _linear_sizes(index, *fields):
 
 
 def _linear_plan(x, weight, activation, generic):
-    """(_linear_sizes, y's shape, N) for x [..., K] and weight [N, K] or [N, 1, 1, K]."""
+    """(device number, _linear_sizes, y's shape, N) for x [..., K] and weight [N, K] or [N, 1, 1, K]."""
     ws, xs = weight.shape, x.shape
     if len(xs) < 1 or len(ws) not in (2, 4) or len(ws) == 4 and (ws[1] != 1 or ws[2] != 1):
         raise ValueError("x must be [..., K] and weight [N, K] or [N, 1, 1, K]")
-    if x.dtype not in _DTYPES:
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
     N, K = ws[0], ws[-1]
     if xs[-1] != K:
         raise ValueError("x must be [..., %d] for weight %s, got %s" % (K, tuple(ws), tuple(xs)))
     if N < 1 or K < 1:
         raise ValueError("weight must not be empty, got %s" % (tuple(ws),))
-    act = _activation(activation)
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor, got %s" % x.device)
-    if x.numel() > _MOST or weight.numel() > _MOST:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _activation(activation)
+    index = _map_device(x)
+    if weight.numel() > _MOST:
         raise ValueError("a tensor exceeds 2^31-1 elements")
-    with _on_device(x):
-        sizes = _linear_sizes(x.device.index, x.numel() // K, N, K, act, _DTYPES[x.dtype],
-                              DCN_FLAG_GENERIC if generic else 0)
-    return sizes, xs[:-1] + (N,), N
+    sizes = _sizes_on(index, _linear_sizes, x.numel() // K, N, K, act, dtype, DCN_FLAG_GENERIC if generic else 0)
+    return index, sizes, xs[:-1] + (N,), N
 
 
 def linear_workspace_size(p: LinearParams, op: int) -> int:
@@ -433,15 +448,19 @@ def linear_forward(x, weight, bias=None, residual=None, activation="none", *, ne
     map, or rows) and weight [N, K] or [N, 1, 1, K]; bias [N], residual [..., N] or None; activation "none",
     "relu", "silu" or "gelu" (with erf). need_preact: (y, z) with the pre-activation z, which the backward pass
     of silu and gelu takes. out: y to write; it may be the residual."""
-    lib = _load()
-    (p, n, _), shape, N = _linear_plan(x, weight, activation, generic)
-    _check_like(x, {"x": x.shape, "weight": weight.shape, "bias": (N,), "residual": shape, "out": shape}, x=x,
-                weight=weight, bias=bias, residual=residual, out=out)
+    lib = _lib or _load()
+    index, (p, n, _), shape, N = _linear_plan(x, weight, activation, generic)
+    dt, dev = x.dtype, x.device
+    if not (x.is_contiguous() and _fits(weight, dt, dev, weight.shape)
+            and (bias is None or _fits(bias, dt, dev, (N,)))
+            and (residual is None or _fits(residual, dt, dev, shape)) and (out is None or _fits(out, dt, dev, shape))):
+        _refuse(dt, dev, x=(x, x.shape), weight=(weight, weight.shape), bias=(bias, (N,)), residual=(residual, shape),
+                out=(out, shape))
     y = x.new_empty(shape) if out is None else out
     z = x.new_empty(shape) if need_preact else None
     ws, wp, n = _scratch(n, x, workspace)
-    _call(lib.dcn_linear_forward, x, p, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(residual), y.data_ptr(),
-          _addr(z), wp, n)
+    _call(lib.dcn_linear_forward, index, p, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(residual),
+          y.data_ptr(), _addr(z), wp, n)
     return (y, z) if need_preact else y
 
 
@@ -450,43 +469,48 @@ def linear_backward(x, weight, saved, grad_y, activation="none", *, need_input=T
     """(grad_x, grad_weight, grad_bias, grad_residual) of linear_forward, entries not requested None. saved: what
     the forward left, y for relu, the pre-activation z for silu and gelu, None for none. grad_x and
     grad_residual have x's dtype, grad_weight (weight's shape) and grad_bias are float32."""
-    lib = _load()
+    lib = _lib or _load()
     if (saved is None) != (activation == "none"):
         raise ValueError("saved must be %s for activation %r" % (
             "None" if activation == "none" else "the output" if activation == "relu" else "the pre-activation",
             activation))
-    (p, _, n), shape, N = _linear_plan(x, weight, activation, generic)
-    _check_like(x, {"x": x.shape, "weight": weight.shape, "saved": shape, "grad_y": shape}, x=x, weight=weight,
-                saved=saved, grad_y=grad_y)
+    index, (p, _, n), shape, N = _linear_plan(x, weight, activation, generic)
+    dt, dev = x.dtype, x.device
+    if not (x.is_contiguous() and _fits(weight, dt, dev, weight.shape) and _fits(grad_y, dt, dev, shape)
+            and (saved is None or _fits(saved, dt, dev, shape))):
+        _refuse(dt, dev, x=(x, x.shape), weight=(weight, weight.shape), saved=(saved, shape), grad_y=(grad_y, shape))
     gx = torch.empty_like(x) if need_input else None
     gw = torch.empty_like(weight, dtype=torch.float32) if need_weight else None
     gb = x.new_empty((N,), dtype=torch.float32) if need_bias else None
     gr = torch.empty_like(grad_y) if need_residual else None
     ws, wp, n = _scratch(n, x, workspace)
-    _call(lib.dcn_linear_backward, x, p, x.data_ptr(), weight.data_ptr(), _addr(saved), grad_y.data_ptr(), _addr(gx),
-          _addr(gw), _addr(gb), _addr(gr), wp, n)
+    _call(lib.dcn_linear_backward, index, p, x.data_ptr(), weight.data_ptr(), _addr(saved), grad_y.data_ptr(),
+          _addr(gx), _addr(gw), _addr(gb), _addr(gr), wp, n)
     return gx, gw, gb, gr
 
 
 @functools.lru_cache(maxsize=1024)
 def _norm_sizes(index, *fields):
-    """(params by reference, forward's and backward's workspace bytes) on the current device, number `index`."""
+    """(params by reference, workspace bytes of the forward and the backward, and of both for aligned maps) on the
+    current device, number `index`."""
     p = NormParams(*fields)
-    return ctypes.byref(p), group_norm_workspace_size(p, OP_FORWARD), group_norm_workspace_size(p, OP_BACKWARD)
+    return (ctypes.byref(p), *(group_norm_workspace_size(p, op | aligned) for aligned in (0, OP_ALIGNED)
+                               for op in (OP_FORWARD, OP_BACKWARD)))
 
 
 def _norm_plan(x, groups, eps, activation):
-    if x.dim() != 4:
+    """(device number, _norm_sizes)"""
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("x must be [B, H, W, C]")
-    if x.dtype not in _DTYPES:
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
-    act = _activation(activation)
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor, got %s" % x.device)
-    if x.numel() > _MOST:
-        raise ValueError("a tensor exceeds 2^31-1 elements")
-    with _on_device(x):
-        return _norm_sizes(x.device.index, *x.shape, int(groups), float(eps), act, _DTYPES[x.dtype], 0)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _activation(activation)
+    index = _map_device(x)
+    return index, _sizes_on(index, _norm_sizes, *shape, groups, float(eps), act, dtype, 0)
 
 
 def group_norm_workspace_size(p: NormParams, op: int) -> int:
@@ -497,16 +521,18 @@ def group_norm_forward(x, gamma, beta, groups, eps=1e-5, activation="none", *, o
     """(y, stats): y = act(gamma (x - mean) rstd + beta) of x [B, H, W, C] over each sample's groups of
     C / groups neighbouring channels, stats float32 [B, groups, 2] = (mean, rstd). gamma, beta [C] or None;
     activation as for linear_forward. out: y to write; it may be x."""
-    lib = _load()
-    p, n, _ = _norm_plan(x, groups, eps, activation)
-    shape = x.shape
+    lib = _lib or _load()
+    index, (p, any_n, _, n, _) = _norm_plan(x, groups, eps, activation)
+    dt, dev, shape = x.dtype, x.device, x.shape
     c = shape[3:]
-    _check_like(x, {"x": shape, "gamma": c, "beta": c, "out": shape}, x=x, gamma=gamma, beta=beta, out=out)
+    if not (x.is_contiguous() and (gamma is None or _fits(gamma, dt, dev, c))
+            and (beta is None or _fits(beta, dt, dev, c)) and (out is None or _fits(out, dt, dev, shape))):
+        _refuse(dt, dev, x=(x, shape), gamma=(gamma, c), beta=(beta, c), out=(out, shape))
     y = torch.empty_like(x) if out is None else out
     stats = x.new_empty((shape[0], max(groups, 0), 2), dtype=torch.float32)
-    ws, wp, n = _scratch(n, x, workspace)
-    _call(lib.dcn_group_norm_forward, x, p, x.data_ptr(), _addr(gamma), _addr(beta), y.data_ptr(), stats.data_ptr(),
-          wp, n)
+    xp, yp = x.data_ptr(), y.data_ptr()
+    ws, wp, n = _scratch(any_n if (xp | yp) & 15 else n, x, workspace)
+    _call(lib.dcn_group_norm_forward, index, p, xp, _addr(gamma), _addr(beta), yp, stats.data_ptr(), wp, n)
     return y, stats
 
 
@@ -514,19 +540,22 @@ def group_norm_backward(x, gamma, beta, stats, grad_y, groups, activation="none"
                         need_params=True, workspace=None):
     """(grad_x, grad_gamma, grad_beta) of group_norm_forward, given its x and stats: grad_x in x's dtype,
     grad_gamma and grad_beta [C] float32, None where gamma or beta is None or not requested."""
-    lib = _load()
-    p, _, n = _norm_plan(x, groups, 1.0, activation)
-    shape = x.shape
+    lib = _lib or _load()
+    index, (p, _, any_n, _, n) = _norm_plan(x, groups, 1.0, activation)
+    dt, dev, shape = x.dtype, x.device, x.shape
     c = shape[3:]
-    _check_like(x, {"x": shape, "gamma": c, "beta": c, "grad_y": shape}, x=x, gamma=gamma, beta=beta, grad_y=grad_y)
-    _check_tensors(torch.float32, x.device, stats=stats)
-    _check_shape("stats", stats, (shape[0], groups, 2))
+    if not (x.is_contiguous() and (gamma is None or _fits(gamma, dt, dev, c))
+            and (beta is None or _fits(beta, dt, dev, c)) and _fits(grad_y, dt, dev, shape)):
+        _refuse(dt, dev, x=(x, shape), gamma=(gamma, c), beta=(beta, c), grad_y=(grad_y, shape))
+    if not _fits(stats, torch.float32, dev, (shape[0], groups, 2)):
+        _refuse(torch.float32, dev, stats=(stats, (shape[0], groups, 2)))
     gx = torch.empty_like(x) if need_input else None
     gg = x.new_empty(c, dtype=torch.float32) if need_params and gamma is not None else None
     gb = x.new_empty(c, dtype=torch.float32) if need_params and beta is not None else None
-    ws, wp, n = _scratch(n, x, workspace)
-    _call(lib.dcn_group_norm_backward, x, p, x.data_ptr(), _addr(gamma), _addr(beta), stats.data_ptr(),
-          grad_y.data_ptr(), _addr(gx), _addr(gg), _addr(gb), wp, n)
+    xp, gp, op = x.data_ptr(), grad_y.data_ptr(), _addr(gx)
+    ws, wp, n = _scratch(any_n if (xp | gp | (op or 0)) & 15 else n, x, workspace)
+    _call(lib.dcn_group_norm_backward, index, p, xp, _addr(gamma), _addr(beta), stats.data_ptr(), gp, op, _addr(gg),
+          _addr(gb), wp, n)
     return gx, gg, gb
 
 

@@ -703,11 +703,13 @@ size_t dcn_group_norm_workspace_size(const dcn_norm_params_t* params, int op) {
         g_err = keep;
         return 0;
     }
-    return dcn::norm_workspace(s, params->dtype == DCN_BF16, op == DCN_OP_BACKWARD);
+    return dcn::norm_workspace(s, params->dtype == DCN_BF16, (op & ~DCN_OP_ALIGNED) == DCN_OP_BACKWARD,
+                               (op & DCN_OP_ALIGNED) != 0);
 }
 
-static int norm_workspace_ok(const dcn_norm_params_t* params, int op, const void* workspace, size_t bytes) {
-    const size_t need = dcn_group_norm_workspace_size(params, op);
+static int norm_workspace_ok(const dcn_norm_params_t* params, int op, bool aligned, const void* workspace,
+                             size_t bytes) {
+    const size_t need = dcn_group_norm_workspace_size(params, op | (aligned ? DCN_OP_ALIGNED : 0));
     if (need > 0 && (!workspace || bytes < need))
         return fail(DCN_ERR_WORKSPACE, "group norm needs %zu bytes of workspace, got %zu", need,
                     workspace ? bytes : (size_t)0);
@@ -725,13 +727,14 @@ int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const
     TRY(check_ptr(beta, "beta", es, false));
     TRY(check_ptr(y, "y", es, true));
     TRY(check_ptr(stats, "stats", 4, false));
-    TRY(norm_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+    const bool aligned = aligned16(x) && aligned16(y);
+    TRY(norm_workspace_ok(params, DCN_OP_FORWARD, aligned, workspace, workspace_bytes));
     unsigned* status = nullptr;
     cudaError_t e = dcn::status_word_ptr(&status);
     if (e != cudaSuccess) return cuda_fail(e, "status word");
     int n = 0;
-    e = dcn::norm_forward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(y), x, gamma, beta, y, stats,
-                          workspace, status, (cudaStream_t)stream, &n);
+    e = dcn::norm_forward(s, params->dtype == DCN_BF16, aligned, x, gamma, beta, y, stats, workspace, status,
+                          (cudaStream_t)stream, &n);
     g_launches += n;
     if (e != cudaSuccess) return cuda_fail(e, "group norm forward launch");
     return ok();
@@ -753,14 +756,14 @@ int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, cons
     TRY(check_ptr(grad_gamma, "grad_gamma", 4, false));
     TRY(check_ptr(grad_beta, "grad_beta", 4, false));
     if (!grad_x && !grad_gamma && !grad_beta) return ok();
-    TRY(norm_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+    const bool aligned = aligned16(x) && aligned16(grad_y) && aligned16(grad_x);
+    TRY(norm_workspace_ok(params, DCN_OP_BACKWARD, aligned, workspace, workspace_bytes));
     unsigned* status = nullptr;
     cudaError_t e = dcn::status_word_ptr(&status);
     if (e != cudaSuccess) return cuda_fail(e, "status word");
     int n = 0;
-    e = dcn::norm_backward(s, params->dtype == DCN_BF16, aligned16(x) && aligned16(grad_y) && aligned16(grad_x), x,
-                           gamma, beta, stats, grad_y, grad_x, grad_gamma, grad_beta, workspace, status,
-                           (cudaStream_t)stream, &n);
+    e = dcn::norm_backward(s, params->dtype == DCN_BF16, aligned, x, gamma, beta, stats, grad_y, grad_x, grad_gamma,
+                           grad_beta, workspace, status, (cudaStream_t)stream, &n);
     g_launches += n;
     if (e != cudaSuccess) return cuda_fail(e, "group norm backward launch");
     return ok();

@@ -741,25 +741,43 @@ cudaError_t backward_t(const NormShape& s, bool vec, const T* x, const T* gamma,
 
 }  // namespace
 
-size_t norm_workspace(const NormShape& s, int bf, bool backward) {
-    size_t most = backward ? (size_t)s.B * s.C * sizeof(float2) : 0;  // by clusters
-    if (norm_stream_supported(s, bf, backward)) most = std::max(most, norm_stream_workspace(s, bf, backward));
-    for (int v : {bf ? 8 : 4, s.C + 1})  // vectors, or (an unaligned map) single values
-        most = std::max(most, space_of(s, make_plan(s, v, bf ? 2 : 4, backward ? 2 : 1), backward).total);
-    return most;
+namespace {
+
+// Which kernels an aligned map goes to. Clusters need one launch; the queue with a ring, two, moves large maps faster:
+// relu on 8x50x50x256 11.5 and 18.5 us, on 8x80x80x256 (26 MB) 27.7 and 25.0 us, on 64x28x28x512 48 and 35 us.
+// (Backward the clusters lead wherever they fit: 64x28x28x512 82 and 118 us.)
+enum class Path { cluster, stream, queue };
+Path path_of(const NormShape& s, int bf, bool backward) {
+    const bool stream = norm_stream_supported(s, bf, backward);
+    const bool large = !backward && (double)s.B * s.HW * s.C * (bf ? 2 : 4) > 24e6 && stream;
+    if (!large && norm_cluster_supported(s, bf, backward)) return Path::cluster;
+    return stream ? Path::stream : Path::queue;
+}
+
+size_t queue_workspace(const NormShape& s, int bf, bool backward, int vec) {
+    return space_of(s, make_plan(s, vec, bf ? 2 : 4, backward ? 2 : 1), backward).total;
+}
+
+}  // namespace
+
+size_t norm_workspace(const NormShape& s, int bf, bool backward, bool aligned) {
+    size_t n = 0;
+    switch (path_of(s, bf, backward)) {
+        case Path::cluster: n = backward ? (size_t)s.B * s.C * sizeof(float2) : 0; break;
+        case Path::stream: n = norm_stream_workspace(s, bf, backward); break;
+        case Path::queue: n = queue_workspace(s, bf, backward, bf ? 8 : 4); break;
+    }
+    return aligned ? n : std::max(n, queue_workspace(s, bf, backward, s.C + 1));  // C + 1: single values
 }
 
 cudaError_t norm_forward(const NormShape& s, int bf, bool vec, const void* x, const void* gamma, const void* beta,
                          void* y, float* stats, void* ws, unsigned* status, cudaStream_t st, int* launches) {
-    // Clusters need one launch; a long queue, two with a ring, moves large maps faster: relu on 8x50x50x256 11.5 and
-    // 18.5 us, on 8x80x80x256 (26 MB) 27.7 and 25.0 us, on 64x28x28x512 48 and 35 us. (Backward the clusters lead
-    // wherever they fit: 64x28x28x512 82 and 118 us.)
-    const bool large = (double)s.B * s.HW * s.C * (bf ? 2 : 4) > 24e6 && norm_stream_supported(s, bf, false);
-    if (vec && !large && norm_cluster_supported(s, bf, false)) {
+    const Path path = vec ? path_of(s, bf, false) : Path::queue;
+    if (path == Path::cluster) {
         ++*launches;
         return norm_cluster_forward(s, bf, x, gamma, beta, y, stats, st);
     }
-    if (vec && norm_stream_supported(s, bf, false)) {
+    if (path == Path::stream) {
         *launches += 2;
         return norm_stream_forward(s, bf, x, gamma, beta, y, stats, ws, status, st);
     }
@@ -772,7 +790,8 @@ cudaError_t norm_forward(const NormShape& s, int bf, bool vec, const void* x, co
 cudaError_t norm_backward(const NormShape& s, int bf, bool vec, const void* x, const void* gamma, const void* beta,
                           const float* stats, const void* gy, void* gx, float* gg, float* gb, void* ws,
                           unsigned* status, cudaStream_t st, int* launches) {
-    if (vec && norm_cluster_supported(s, bf, true)) {
+    const Path path = vec ? path_of(s, bf, true) : Path::queue;
+    if (path == Path::cluster) {
         float2* sums = gg || gb ? (float2*)ws : nullptr;
         cudaError_t e = norm_cluster_backward(s, bf, x, gamma, beta, stats, gy, sums, gx, st);
         if (e != cudaSuccess) return e;
@@ -783,7 +802,7 @@ cudaError_t norm_backward(const NormShape& s, int bf, bool vec, const void* x, c
         }
         return e;
     }
-    if (vec && norm_stream_supported(s, bf, true)) {
+    if (path == Path::stream) {
         *launches += 2;
         return norm_stream_backward(s, bf, x, gamma, beta, stats, gy, gx, gg, gb, ws, status, st);
     }

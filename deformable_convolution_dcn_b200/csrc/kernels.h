@@ -142,7 +142,8 @@ struct NormShape {
     int B, HW, C, groups, act;
     float eps;
 };
-size_t norm_workspace(const NormShape& s, int dtype_bf16, bool backward);
+// aligned: what is enough where vec will be true
+size_t norm_workspace(const NormShape& s, int dtype_bf16, bool backward, bool aligned);
 cudaError_t norm_forward(const NormShape& s, int dtype_bf16, bool vec, const void* x, const void* gamma,
                          const void* beta, void* y, float* stats, void* ws, unsigned* status, cudaStream_t st,
                          int* launches);

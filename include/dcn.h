@@ -307,7 +307,10 @@ typedef struct {
 } dcn_norm_params_t;
 
 /* Bytes of workspace (16-byte aligned) of the forward (op DCN_OP_FORWARD) or the
- * backward (DCN_OP_BACKWARD); 0 for invalid params. */
+ * backward (DCN_OP_BACKWARD), whatever the maps' alignment; op | DCN_OP_ALIGNED:
+ * what is enough (often 0) where x, y, grad_y and grad_x are all 16-byte
+ * aligned. 0 for invalid params. */
+#define DCN_OP_ALIGNED 0x100
 DCN_API size_t dcn_group_norm_workspace_size(const dcn_norm_params_t* params, int op);
 
 /* Writes y, and stats unless it is NULL. y may be x. */

@@ -216,6 +216,12 @@ def test_group_norm_refusals_on_the_device():
         dcn.group_norm_backward(d["x"], None, None, torch.zeros(2, 3, 2, device="cuda"), d["gy"], 4)
     ws = torch.empty(8, dtype=torch.uint8, device="cuda")
     p = dcn.NormParams(2, 4, 4, 16, 4, EPS, 0, dcn.DCN_BF16, 0)
-    if dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD) > 8:
-        with pytest.raises(dcn.DcnError, match="workspace"):
-            dcn.group_norm_backward(d["x"], None, None, given_stats(d, 4), d["gy"], 4, workspace=ws)
+    assert dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD | dcn.OP_ALIGNED) > 8
+    with pytest.raises(dcn.DcnError, match="workspace"):
+        dcn.group_norm_backward(d["x"], None, None, given_stats(d, 4), d["gy"], 4, workspace=ws)
+    # a small aligned map takes none forward; the same map off its alignment does
+    assert dcn.group_norm_workspace_size(p, dcn.OP_FORWARD | dcn.OP_ALIGNED) == 0
+    dcn.group_norm_forward(d["x"], None, None, 4, workspace=ws)
+    off = torch.cat([d["x"].flatten()[:1], d["x"].flatten()])[1:].view(d["x"].shape)
+    with pytest.raises(dcn.DcnError, match="workspace"):
+        dcn.group_norm_forward(off, None, None, 4, workspace=ws)

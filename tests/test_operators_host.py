@@ -108,8 +108,11 @@ def test_group_norm_pointers_and_workspace(lib):
     for kw in (dict(x=None), dict(st=None), dict(gy=None)):
         assert gn_bwd(lib, p, **kw) == EINVAL
     assert gn_bwd(lib, p, gx=None, gg=None, gb=None) == OK
-    for op, call in ((dcn.OP_FORWARD, gn_fwd), (dcn.OP_BACKWARD, gn_bwd)):
+    off = ctypes.c_void_p((1 << 20) + 2)
+    for op, call in ((dcn.OP_FORWARD, lambda *a, **k: gn_fwd(*a, x=off, **k)),
+                     (dcn.OP_BACKWARD, lambda *a, **k: gn_bwd(*a, x=off, **k))):
         n = dcn.group_norm_workspace_size(p, op)
+        assert n >= dcn.group_norm_workspace_size(p, op | dcn.OP_ALIGNED)
         if n:
             assert call(lib, p, ws=None) == EWS
             assert call(lib, p, n=n - 1) == EWS
