@@ -53,6 +53,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 }
 
 const long long kMaxElems = (1LL << 31) - 1;
+const long long kMaxDim = 1LL << 30;  // rows of a matrix, pixels of a map: a tile past the end stays an int
 
 // Validates params and fills the kernel-side shape. Returns DCN_OK or an error code (message set).
 int make_shape(const dcn_params_t* p, dcn::Shape& s) {
@@ -567,6 +568,8 @@ static int linear_shape(const dcn_linear_params_t* p, dcn::LinearShape& s) {
     if (p->dtype != DCN_F32 && p->dtype != DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "unknown dtype %d", p->dtype);
     if ((long long)p->M * p->K > kMaxElems || (long long)p->M * p->N > kMaxElems || (long long)p->N * p->K > kMaxElems)
         return fail(DCN_ERR_UNSUPPORTED, "a tensor exceeds 2^31-1 elements");
+    if (p->M > kMaxDim || p->N > kMaxDim || p->K > kMaxDim)
+        return fail(DCN_ERR_UNSUPPORTED, "a dimension exceeds 2^30 (M=%d N=%d K=%d)", p->M, p->N, p->K);
     s.M = p->M;
     s.N = p->N;
     s.K = p->K;
@@ -687,6 +690,9 @@ static int norm_shape(const dcn_norm_params_t* p, dcn::NormShape& s) {
     if (p->dtype != DCN_F32 && p->dtype != DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "unknown dtype %d", p->dtype);
     if ((double)p->B * p->H * p->W * p->C > (double)kMaxElems)
         return fail(DCN_ERR_UNSUPPORTED, "a tensor exceeds 2^31-1 elements");
+    if ((long long)p->H * p->W > kMaxDim || (long long)p->B * p->groups > kMaxDim / 4)
+        return fail(DCN_ERR_UNSUPPORTED, "H*W up to 2^30 and B*groups up to 2^28 (B=%d H=%d W=%d groups=%d)", p->B, p->H,
+                    p->W, p->groups);
     s.B = p->B;
     s.HW = p->H * p->W;
     s.C = p->C;

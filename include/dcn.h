@@ -259,7 +259,7 @@ typedef enum {
  * rounded once each. float32 layers keep float32 accuracy on the tensor cores
  * (operands split in three bfloat16 terms). Infinities and NaN of a bfloat16
  * layer spread as in the sums above; a float32 layer may turn an infinity into
- * NaN. M may be 0. */
+ * NaN. M may be 0; M, N, K up to 2^30, each tensor below 2^31 elements. */
 typedef struct {
     int M, N, K;
     int act;         /* dcn_act_t */
@@ -296,7 +296,8 @@ DCN_API int dcn_linear_backward(const dcn_linear_params_t* params, const void* x
  *   x, y [B, H, W, C], gamma, beta [C] or NULL (1 and 0), all in `dtype`;
  *   stats [B, groups, 2] float32: (mean, rstd).
  * Arithmetic is float32. A group that holds an infinity or a NaN becomes NaN;
- * other groups do not notice. */
+ * other groups do not notice. H*W up to 2^30, B*groups up to 2^28, each tensor
+ * below 2^31 elements. */
 typedef struct {
     int B, H, W, C;
     int groups;      /* C % groups == 0 */

@@ -52,7 +52,8 @@ def gn_bwd(lib, p, x=F, ga=None, be=None, st=F, gy=F, gx=F, gg=F, gb=F, ws=F, n=
 @pytest.mark.parametrize("bad,code", [
     (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=0), EINVAL), (dict(act=4), EINVAL), (dict(act=-1), EINVAL),
     (dict(dtype=2), EUNSUP), (dict(M=1 << 20, N=1 << 12), EUNSUP), (dict(M=1 << 20, K=1 << 12), EUNSUP),
-    (dict(N=1 << 20, K=1 << 12), EUNSUP),
+    (dict(N=1 << 20, K=1 << 12), EUNSUP), (dict(M=(1 << 30) + 1, N=1, K=1), EUNSUP),
+    (dict(M=1, N=1, K=(1 << 30) + 1), EUNSUP),
 ])
 def test_linear_params_rejected(lib, bad, code):
     p = LP(**bad)
@@ -88,7 +89,8 @@ def test_linear_without_rows_or_outputs_enqueues_nothing(lib):
     (dict(B=0), EINVAL), (dict(H=0), EINVAL), (dict(W=-2), EINVAL), (dict(C=0), EINVAL), (dict(groups=0), EINVAL),
     (dict(groups=5), EINVAL), (dict(eps=0.0), EINVAL), (dict(eps=float("nan")), EINVAL),
     (dict(eps=float("inf")), EINVAL), (dict(act=9), EINVAL), (dict(dtype=3), EUNSUP),
-    (dict(B=1 << 10, H=1 << 10, W=1 << 10), EUNSUP),
+    (dict(B=1 << 10, H=1 << 10, W=1 << 10), EUNSUP), (dict(B=1, H=1 << 16, W=(1 << 14) + 1, C=1, groups=1), EUNSUP),
+    (dict(B=(1 << 28) + 1, H=1, W=1, C=1, groups=1), EUNSUP),
 ])
 def test_group_norm_params_rejected(lib, bad, code):
     p = NP(**bad)
