@@ -585,6 +585,8 @@ size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op) {
         return 0;
     }
     if ((params->flags & DCN_FLAG_GENERIC) || s.M == 0) return 0;
+    // a few rows whose base is unaligned take the generic kernel, which needs none either
+    if (op != DCN_OP_BACKWARD && dcn::linear_few_supported(s, params->dtype == DCN_BF16)) return 0;
     return dcn::linear_tc_workspace(s, params->dtype == DCN_BF16, op == DCN_OP_BACKWARD);
 }
 
@@ -620,7 +622,15 @@ int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const v
     TRY(check_ptr(z, "z", es, false));
     if (!any) return ok();
     int n = 0;
-    if (use_linear_tc(params, s, x, weight, nullptr)) {
+    const bool few = dcn::linear_few_supported(s, params->dtype == DCN_BF16);
+    if (few && !(params->flags & DCN_FLAG_GENERIC) && aligned16(x) && aligned16(weight)) {
+        cudaError_t e = dcn::linear_few_forward(s, params->dtype == DCN_BF16, x, weight, bias, residual, y, z,
+                                                (cudaStream_t)stream);
+        g_launches += 1;
+        if (e != cudaSuccess) return cuda_fail(e, "linear forward launch");
+        return ok();
+    }
+    if (!few && use_linear_tc(params, s, x, weight, nullptr)) {
         TRY(linear_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
         unsigned* status = nullptr;
         cudaError_t e = dcn::status_word_ptr(&status);

@@ -136,6 +136,11 @@ cudaError_t linear_tc_backward(const LinearShape& s, int dtype_bf16, const void*
 // x and w (in_gy: grad_y) are read in place, not through a copy in the workspace.
 void linear_tc_in_place(const LinearShape& s, int dtype_bf16, bool* in_xw, bool* in_gy);
 
+// linear_few.cu — the forward for a few rows, bound by the weight's bytes (x and w 16-byte aligned).
+bool linear_few_supported(const LinearShape& s, int dtype_bf16);
+cudaError_t linear_few_forward(const LinearShape& s, int dtype_bf16, const void* x, const void* w, const void* bias,
+                               const void* residual, void* y, void* z, cudaStream_t st);
+
 // group_norm.cu — group normalisation with an activation, channels last. vec: x, y, grad_y and
 // grad_x are 16-byte aligned.
 struct NormShape {

@@ -15,7 +15,9 @@ ACTS = ("none", "relu", "silu", "gelu")
 # reduction), several tiles in every direction, an output of one column
 SIZES = [(1, 1, 1), (1, 8, 8), (3, 7, 5), (2, 1, 300), (17, 33, 65), (64, 64, 64), (128, 128, 64), (129, 136, 72),
          (200, 257, 130), (1000, 64, 24), (5, 1024, 520), (33, 24, 4104), (300, 72, 2056), (2500, 40, 48),
-         (777, 520, 264), (4099, 16, 8), (260, 1032, 96)]
+         (777, 520, 264), (4099, 16, 8), (260, 1032, 96),
+         # a few rows: every count of them, weights of one row and of more than the GPU has blocks for
+         (1, 1024, 2056), (2, 81, 1024), (3, 600, 64), (4, 1, 8), (6, 2001, 264), (7, 593, 4), (8, 331, 12544), (9, 331, 512)]
 
 
 def make(M, N, K, dtype, bias=True, residual=True, seed=0, device="cuda"):
