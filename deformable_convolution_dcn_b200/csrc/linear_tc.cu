@@ -55,6 +55,12 @@ struct Operand {
     int kind;
 };
 
+// grad_bias from the column sums of row blocks (gb null: not asked for).
+struct Sums {
+    const float* sums;
+    int blocks, pitch, n;
+    float* gb;
+};
 struct GemmArgs {
     int rows, cols;        // D: A-side rows, B-side rows
     int kblocks, splits;   // stages of 64; parts along the reduction
@@ -74,6 +80,7 @@ struct GemmArgs {
     int nslots;            // chunks a warp stages (tma_out)
     uint32_t slot_off, sm_off;  // the epilogue's slots or exchange buffers; its bias
     unsigned* status;
+    Sums gb;               // grad_bias, joined by the epilogue warps while they wait for the first accumulator
 };
 
 // Shared-memory descriptors of one operand's tiles. Only the start address (the low word, in 16-byte units) changes
@@ -273,6 +280,35 @@ struct Emit {
     }
 };
 
+// grad_bias of one chunk of eight columns a warp: two threads' four columns, 16 threads' rows, joined in a fixed order.
+// The sums are a few MB at most, and the warps that join them would wait for a product's first accumulator meanwhile: a
+// launch of its own made the backward pass of 5000x2048x512 9 us longer. (Rows of `pitch`, a multiple of 8, are written
+// to their ends.)
+__device__ __forceinline__ void join_bias(const Sums& s, int chunk, int chunks, int lane) {
+    for (; chunk * 8 < s.n; chunk += chunks) {
+        const int n = chunk * 8 + lane % 2 * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 12
+        for (int i = lane / 2; i < s.blocks; i += 16) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(s.sums + (long long)i * s.pitch + n));
+            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+#pragma unroll
+        for (int d = 2; d < 32; d *= 2) {
+            v.x += __shfl_xor_sync(~0u, v.x, d);
+            v.y += __shfl_xor_sync(~0u, v.y, d);
+            v.z += __shfl_xor_sync(~0u, v.z, d);
+            v.w += __shfl_xor_sync(~0u, v.w, d);
+        }
+        // gb has no alignment of its own to rely on
+        if (lane < 8) {
+            const int k = lane / 2;
+            const float one = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+            if (n + k < s.n) s.gb[n + k] = one;
+        }
+    }
+}
+
 // T: element type of D. PB: 0, or BN where the accumulator is added up in registers.
 template <typename T, int PB, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -433,9 +469,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     const uint32_t more = k ? 1u : first;
                                     const uint64_t a0 = da.at(off, k), b0 = db.at(off, k);
                                     ptx::mma_bf16_cg<CG>(acc, a0, b0, idesc, more);
-                                    ptx::mma_bf16_cg<CG>(low, da.at(off + 2 * aterm, k), b0, idesc, more);
                                     const uint64_t a1 = da.at(off + aterm, k);
-                                    ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, 1u);
+                                    ptx::mma_bf16_cg<CG>(low, a1, b0, idesc, more);
+                                    ptx::mma_bf16_cg<CG>(low, da.at(off + 2 * aterm, k), b0, idesc, 1u);
                                     if (both) {
                                         const uint64_t b1 = db.at(off + bterm, k);
                                         ptx::mma_bf16_cg<CG>(low, a0, db.at(off + 2 * bterm, k), idesc, 1u);
@@ -495,6 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             buf ^= 1;
             phase ^= buf ^ 1;
         };
+        if (a.gb.gb) join_bias(a.gb, w * gridDim.x + blockIdx.x, EPI_WARPS * gridDim.x, lane);
         // the residual's cursor: the next chunk to fetch, nslots - 1 ahead of the one written
         const bool has_res = a.residual && a.tma_out;
         int fu = group, fc = 0;
@@ -609,8 +646,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // -------------------------------------------------- after the products --
 
-// What remains after a product: a split reduction's parts to be joined, and grad_bias from the column sums of row
-// blocks. One kernel does both (either may be absent), so that neither waits for the other's launch.
+// What remains after a split reduction: its parts are joined.
 template <typename T>
 struct FinishArgs {
     // D[m, n] = sum of the parts (in order), then the epilogue; four columns a thread
@@ -620,36 +656,17 @@ struct FinishArgs {
     const T *bias, *residual;
     T *y, *z;
     int act;
-    // gb[n] = sum of sums[block][n]: 32 columns and eight lanes a block
-    const float* sums;
-    int sum_blocks, sum_pitch, sum_n, gb_blocks;
-    float* gb;
 };
 
 constexpr int FINISH_THREADS = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const FinishArgs<T> a) {
-    __shared__ float sm[FINISH_THREADS / 32][33];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if ((int)blockIdx.x < a.gb_blocks) {
-        const int q = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + q;
-        float v = 0.f;
-        if (n < a.sum_n)
-#pragma unroll 16
-            for (int i = l; i < a.sum_blocks; i += FINISH_THREADS / 32) v += a.sums[(long long)i * a.sum_pitch + n];
-        sm[l][q] = v;
-        __syncthreads();
-        if (l == 0 && n < a.sum_n) {
-            for (int i = 1; i < FINISH_THREADS / 32; ++i) v += sm[i][q];
-            a.gb[n] = v;
-        }
-        return;
-    }
     const int n4 = (a.N + 3) / 4;
     const long long total = (long long)a.M * n4;
-    for (long long i = (blockIdx.x - a.gb_blocks) * (long long)FINISH_THREADS + threadIdx.x; i < total;
+    for (long long i = blockIdx.x * (long long)FINISH_THREADS + threadIdx.x; i < total;
          i += (long long)a.part_blocks * FINISH_THREADS) {
         const long long m = i / n4;
         const int n = (int)(i - m * n4) * 4;
@@ -671,6 +688,13 @@ __global__ void __launch_bounds__(FINISH_THREADS) finish_kernel(const FinishArgs
                 a.y[at] = from_float<T>(act_run<kFast<T>>(s, a.act));
             }
     }
+}
+
+// grad_bias by itself, where no product is asked for.
+__global__ void __launch_bounds__(32) bias_kernel(const Sums s) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    join_bias(s, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 // ----------------------------------------------------- operand preparation --
@@ -815,6 +839,8 @@ __device__ __forceinline__ void run_pack(const PackJob<T>& j, int block) {
     }
 }
 
+constexpr int SUM_PITCH = 260;  // of a block's partial column sums: no bank conflicts, written or read
+
 template <typename T, int ACT, int TERMS, bool VEC>
 __device__ __forceinline__ void run_dz(const DzJob<T>& j, int block, float* sm) {
     const int c8 = j.pitch / 8;
@@ -845,22 +871,20 @@ __device__ __forceinline__ void run_dz(const DzJob<T>& j, int block, float* sm) 
     }
     if (!j.sums) return;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sm[threadIdx.x * 8 + q] = sum[q];
+    for (int q = 0; q < 8; ++q) sm[q * SUM_PITCH + threadIdx.x] = sum[q];
     __syncthreads();
-    if (ry == 0 && c < j.pitch) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float v = 0.f;
-            for (int r = 0; r < ty; ++r) v += sm[(r * tx + cx) * 8 + q];
-            j.sums[(long long)rb * j.pitch + c + q] = v;
-        }
+    const int c0 = (block % j.cblocks) * tx * 8;
+    for (int i = threadIdx.x; i < tx * 8; i += 256) {  // a column each
+        float v = 0.f;
+        for (int r = 0; r < ty; ++r) v += sm[(i % 8) * SUM_PITCH + r * tx + i / 8];
+        if (c0 + i < j.pitch) j.sums[(long long)rb * j.pitch + c0 + i] = v;
     }
 }
 
 // All of a call's operand preparation in one launch.
 template <typename T, int ACT, int TERMS>
 __global__ void __launch_bounds__(256) prep_kernel(const DzJob<T> dz, const PackJob<T> a, const PackJob<T> b) {
-    __shared__ float sm[256 * 8];
+    __shared__ float sm[SUM_PITCH * 8];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int block = blockIdx.x;
@@ -961,7 +985,7 @@ struct GemmPlan {
 GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool f32_out, int out_bytes, int act) {
     const int kblocks = (red + BK - 1) / BK;
     const int sms = num_sms();
-    const int prods = ta == 1 ? 1 : tb == 1 ? 3 : 6;
+    const int prods = tb == 1 ? ta : 6;
     const double element = out_bytes / 24.0 + (act == kActSilu || act == kActGelu ? 0.2 : 0.0);
     GemmPlan best = {};
     double best_t = 1e300;
@@ -1021,29 +1045,13 @@ size_t part_bytes(const GemmPlan& p, long long rows, long long cols) {
     return p.splits > 1 ? (size_t)p.splits * rows * ((cols + 7) / 8 * 8) * 4 : 0;
 }
 
-// grad_bias from the column sums of row blocks (gb null: not asked for).
-struct Sums {
-    const float* sums;
-    int blocks, pitch, n;
-    float* gb;
-};
-template <typename T>
-void bias_job(FinishArgs<T>& f, const Sums& s) {
-    if (!s.gb) return;
-    f.sums = s.sums;
-    f.sum_blocks = s.blocks;
-    f.sum_pitch = s.pitch;
-    f.sum_n = s.n;
-    f.gb = s.gb;
-    f.gb_blocks = (s.n + 31) / 32;
-}
 template <typename T>
 cudaError_t finish(const FinishArgs<T>& f, cudaStream_t st, int* launches) {
     ++*launches;
-    return launch(finish_kernel<T>, f.gb_blocks + f.part_blocks, FINISH_THREADS, 0, 1, st, f);
+    return launch(finish_kernel<T>, f.part_blocks, FINISH_THREADS, 0, 1, st, f);
 }
 
-// D [rows, cols] (rows of `cols`) = A B^T through the epilogue, and (sums) grad_bias after it. A: K-major [rows, red], or (a_mn) [red, rows]; B alike
+// D [rows, cols] (rows of `cols`) = A B^T through the epilogue, and (sums) grad_bias beside it. A: K-major [rows, red], or (a_mn) [red, rows]; B alike
 // with cols. `parts`: room for the split reduction's results.
 template <typename T>
 cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix& B, bool b_mn, int rows, int cols,
@@ -1066,6 +1074,7 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.b.terms = R.terms;
     a.stage_bytes = L.terms * A_BYTES + R.terms * (uint32_t)(p.bn / p.cg) * 128;
     a.status = status;
+    a.gb = sums;
     const bool split = p.splits > 1;
     const int pitch = split ? (cols + 7) / 8 * 8 : cols;
     a.rs = p.swap ? 1 : pitch;
@@ -1142,12 +1151,6 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
         f.y = out.y;
         f.z = out.z;
         f.act = out.act;
-        bias_job(f, sums);
-        return finish(f, st, launches);
-    }
-    if (sums.gb) {
-        FinishArgs<T> f = {};
-        bias_job(f, sums);
         return finish(f, st, launches);
     }
     return cudaSuccess;
@@ -1185,6 +1188,11 @@ struct BwdPlan {
     GemmPlan gx, gw;
     size_t x, w, dz, sums, parts, total;
 };
+// How many bfloat16 terms of dz grad_weight, a float32 result, takes. dz is exact in one where it is grad_y or 0.
+// (Two for silu and gelu leave out 2^-18 of it: 5000x2048x512 took 67.6 us without grad_bias, with three 73.5, but
+// grad_weight was 10 times as far from the exact one.)
+constexpr int dz_terms(int bf, bool smooth) { return bf && !smooth ? 1 : 3; }
+
 BwdPlan plan_backward(const LinearShape& s, int bf) {
     BwdPlan p = {};
     const int terms = bf ? 1 : 3;
@@ -1193,9 +1201,7 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
     linear_tc_in_place(s, bf, &xw, &gy);
     p.pack_x = p.pack_w = !xw;
     p.pass_dz = !gy;
-    // dz is exact in one bfloat16 term where it is grad_y or 0; grad_weight, a float32 result, takes three of the
-    // others
-    p.dz_terms = bf && !smooth ? 1 : 3;
+    p.dz_terms = dz_terms(bf, smooth);
     // grad_x of a bfloat16 layer reads the first term alone: dz rounded once, as a grad_x in bfloat16 is
     p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4, kActNone);
     p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4, kActNone);
@@ -1237,8 +1243,7 @@ cudaError_t prepare(int act, const DzJob<T>& dz, const PackJob<T>& a, const Pack
     ++*launches;
     return with_act(dz.blocks ? act : kActNone, [&](auto A) {
         constexpr int ACT = decltype(A)::value;
-        // as BwdPlan::dz_terms
-        constexpr int TERMS = std::is_same<T, bf16>::value && (ACT == kActNone || ACT == kActRelu) ? 1 : 3;
+        constexpr int TERMS = dz_terms(std::is_same<T, bf16>::value, ACT == kActSilu || ACT == kActGelu);
         return launch(prep_kernel<T, ACT, TERMS>, blocks, 256, 0, 1, st, dz, a, b);
     });
 }
@@ -1304,9 +1309,8 @@ cudaError_t backward_t(const LinearShape& s, const T* x, const T* w, const T* sa
                                Out<float>{nullptr, nullptr, gw, nullptr, kActNone}, (float*)(ws + p.parts), true, sums,
                                status, st, launches);
     if (gb && !gx) {
-        FinishArgs<T> f = {};
-        bias_job(f, sums);
-        return finish(f, st, launches);
+        ++*launches;
+        return launch(bias_kernel, std::min((s.N + 7) / 8, 1 << 16), 32, 0, 1, st, sums);
     }
     return cudaSuccess;
 }
