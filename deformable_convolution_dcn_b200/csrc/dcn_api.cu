@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <string>
 
 #include "dcn.h"
@@ -107,6 +108,30 @@ int check_ptr(const void* ptr, const char* name, size_t align, bool required) {
     if (!ptr) return required ? fail(DCN_ERR_INVALID_ARG, "%s is NULL", name) : DCN_OK;
     if ((uintptr_t)ptr % align)
         return fail(DCN_ERR_UNSUPPORTED, "%s is not aligned to %zu bytes", name, align);
+    return DCN_OK;
+}
+
+// A buffer of a call: name, address (may be NULL) and bytes.
+struct Buf {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+
+// Refuses outputs that share memory with an input or with each other. in_place: the first output may be the first
+// input.
+int check_apart(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins, bool in_place) {
+    auto meet = [](const Buf& a, const Buf& b) {
+        const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
+        return a.p && b.p && p < q + b.bytes && q < p + a.bytes;
+    };
+    for (const Buf* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Buf* i = ins.begin(); i != ins.end(); ++i)
+            if (meet(*o, *i) && !(in_place && o == outs.begin() && i == ins.begin() && o->p == i->p))
+                return fail(DCN_ERR_INVALID_ARG, "%s overlaps %s", o->name, i->name);
+        for (const Buf* i = o + 1; i != outs.end(); ++i)
+            if (meet(*o, *i)) return fail(DCN_ERR_INVALID_ARG, "%s overlaps %s", o->name, i->name);
+    }
     return DCN_OK;
 }
 
@@ -623,6 +648,17 @@ int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const v
     if (!any) return ok();
     int n = 0;
     const bool few = dcn::linear_few_supported(s, params->dtype == DCN_BF16);
+    const bool tc = !few && use_linear_tc(params, s, x, weight, nullptr);
+    if (tc) TRY(linear_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+    const size_t mn = (size_t)s.M * s.N * es;
+    TRY(check_apart({{"y", y, mn},
+                     {"z", z, mn},
+                     {"workspace", workspace, tc ? dcn_linear_workspace_size(params, DCN_OP_FORWARD) : 0}},
+                    {{"residual", residual, mn},
+                     {"x", x, (size_t)s.M * s.K * es},
+                     {"weight", weight, (size_t)s.N * s.K * es},
+                     {"bias", bias, s.N * es}},
+                    true));
     if (few && !(params->flags & DCN_FLAG_GENERIC) && aligned16(x) && aligned16(weight)) {
         cudaError_t e = dcn::linear_few_forward(s, params->dtype == DCN_BF16, x, weight, bias, residual, y, z,
                                                 (cudaStream_t)stream);
@@ -630,8 +666,7 @@ int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const v
         if (e != cudaSuccess) return cuda_fail(e, "linear forward launch");
         return ok();
     }
-    if (!few && use_linear_tc(params, s, x, weight, nullptr)) {
-        TRY(linear_workspace_ok(params, DCN_OP_FORWARD, workspace, workspace_bytes));
+    if (tc) {
         unsigned* status = nullptr;
         cudaError_t e = dcn::status_word_ptr(&status);
         if (e != cudaSuccess) return cuda_fail(e, "status word");
@@ -667,8 +702,20 @@ int dcn_linear_backward(const dcn_linear_params_t* params, const void* x, const 
     if (!grad_x && !grad_weight && !grad_bias && !grad_residual) return ok();
     if (!any) grad_x = nullptr, grad_residual = nullptr;  // no rows; grad_weight and grad_bias are zero
     int n = 0;
-    if (any && use_linear_tc(params, s, x, weight, grad_y)) {
-        TRY(linear_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+    const bool tc = any && use_linear_tc(params, s, x, weight, grad_y);
+    if (tc) TRY(linear_workspace_ok(params, DCN_OP_BACKWARD, workspace, workspace_bytes));
+    const size_t mn = (size_t)s.M * s.N * es, mk = (size_t)s.M * s.K * es;
+    TRY(check_apart({{"grad_x", grad_x, mk},
+                     {"grad_weight", grad_weight, (size_t)s.N * s.K * 4},
+                     {"grad_bias", grad_bias, (size_t)s.N * 4},
+                     {"grad_residual", grad_residual, mn},
+                     {"workspace", workspace, tc ? dcn_linear_workspace_size(params, DCN_OP_BACKWARD) : 0}},
+                    {{"x", x, mk},
+                     {"weight", weight, (size_t)s.N * s.K * es},
+                     {"saved", saved, mn},
+                     {"grad_y", grad_y, mn}},
+                    false));
+    if (tc) {
         unsigned* status = nullptr;
         cudaError_t e = dcn::status_word_ptr(&status);
         if (e != cudaSuccess) return cuda_fail(e, "status word");
@@ -745,6 +792,12 @@ int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const
     TRY(check_ptr(stats, "stats", 4, false));
     const bool aligned = aligned16(x) && aligned16(y);
     TRY(norm_workspace_ok(params, DCN_OP_FORWARD, aligned, workspace, workspace_bytes));
+    const size_t map = (size_t)s.B * s.HW * s.C * es;
+    const int op = DCN_OP_FORWARD | (aligned ? DCN_OP_ALIGNED : 0);
+    TRY(check_apart({{"y", y, map},
+                     {"stats", stats, (size_t)s.B * s.groups * 8},
+                     {"workspace", workspace, dcn_group_norm_workspace_size(params, op)}},
+                    {{"x", x, map}, {"gamma", gamma, s.C * es}, {"beta", beta, s.C * es}}, true));
     unsigned* status = nullptr;
     cudaError_t e = dcn::status_word_ptr(&status);
     if (e != cudaSuccess) return cuda_fail(e, "status word");
@@ -774,6 +827,18 @@ int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, cons
     if (!grad_x && !grad_gamma && !grad_beta) return ok();
     const bool aligned = aligned16(x) && aligned16(grad_y) && aligned16(grad_x);
     TRY(norm_workspace_ok(params, DCN_OP_BACKWARD, aligned, workspace, workspace_bytes));
+    const size_t map = (size_t)s.B * s.HW * s.C * es;
+    const int back = DCN_OP_BACKWARD | (aligned ? DCN_OP_ALIGNED : 0);
+    TRY(check_apart({{"grad_x", grad_x, map},
+                     {"grad_gamma", grad_gamma, (size_t)s.C * 4},
+                     {"grad_beta", grad_beta, (size_t)s.C * 4},
+                     {"workspace", workspace, dcn_group_norm_workspace_size(params, back)}},
+                    {{"grad_y", grad_y, map},
+                     {"x", x, map},
+                     {"gamma", gamma, s.C * es},
+                     {"beta", beta, s.C * es},
+                     {"stats", stats, (size_t)s.B * s.groups * 8}},
+                    true));
     unsigned* status = nullptr;
     cudaError_t e = dcn::status_word_ptr(&status);
     if (e != cudaSuccess) return cuda_fail(e, "status word");

@@ -272,7 +272,7 @@ typedef struct {
 DCN_API size_t dcn_linear_workspace_size(const dcn_linear_params_t* params, int op);
 
 /* Writes y, and z [M, N] in `dtype` unless it is NULL. y and z must not overlap
- * an input, but y may be the residual. */
+ * an input or each other (DCN_ERR_INVALID_ARG), but y may be the residual. */
 DCN_API int dcn_linear_forward(const dcn_linear_params_t* params, const void* x, const void* weight, const void* bias,
                                const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
                                void* stream);
@@ -283,7 +283,8 @@ DCN_API int dcn_linear_forward(const dcn_linear_params_t* params, const void* x,
  *   next call's grad_y), grad_weight [N, K] = dz^T x and grad_bias [N] = the
  *   column sums of dz in float32.
  * Each output may be NULL (not computed); x may be NULL without grad_weight,
- * weight without grad_x. relu has slope 0 at 0. Equal calls give equal bits. */
+ * weight without grad_x. relu has slope 0 at 0. Equal calls give equal bits.
+ * The outputs must overlap neither an input nor each other (DCN_ERR_INVALID_ARG). */
 DCN_API int dcn_linear_backward(const dcn_linear_params_t* params, const void* x, const void* weight,
                                 const void* saved, const void* grad_y, void* grad_x, float* grad_weight,
                                 float* grad_bias, void* grad_residual, void* workspace, size_t workspace_bytes,
@@ -314,7 +315,8 @@ typedef struct {
 #define DCN_OP_ALIGNED 0x100
 DCN_API size_t dcn_group_norm_workspace_size(const dcn_norm_params_t* params, int op);
 
-/* Writes y, and stats unless it is NULL. y may be x. */
+/* Writes y, and stats unless it is NULL. y may be x; other overlaps of an output
+ * are refused (DCN_ERR_INVALID_ARG). */
 DCN_API int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* x, const void* gamma,
                                    const void* beta, void* y, float* stats, void* workspace, size_t workspace_bytes,
                                    void* stream);
@@ -322,7 +324,7 @@ DCN_API int dcn_group_norm_forward(const dcn_norm_params_t* params, const void* 
 /* Given grad_y [B, H, W, C] (dtype) and the forward's x and stats: grad_x in
  * `dtype` (the gradient through mean and rstd included), grad_gamma and
  * grad_beta [C] in float32. Each output may be NULL (not computed); grad_x may be
- * grad_y. relu has slope 0 at 0. Equal calls give equal bits. */
+ * grad_y, and other overlaps are refused. relu has slope 0 at 0. Equal calls give equal bits. */
 DCN_API int dcn_group_norm_backward(const dcn_norm_params_t* params, const void* x, const void* gamma,
                                     const void* beta, const float* stats, const void* grad_y, void* grad_x,
                                     float* grad_gamma, float* grad_beta, void* workspace, size_t workspace_bytes,

@@ -225,3 +225,36 @@ def test_group_norm_refusals_on_the_device():
     off = torch.cat([d["x"].flatten()[:1], d["x"].flatten()])[1:].view(d["x"].shape)
     with pytest.raises(dcn.DcnError, match="workspace"):
         dcn.group_norm_forward(off, None, None, 4, workspace=ws)
+
+
+# a cluster's map, one of the ring, one of single values
+@pytest.mark.parametrize("size", [(2, 20, 21, 64, 8), (3, 129, 131, 96, 32), (3, 129, 131, 33, 3)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_group_norm_in_place_on_every_path(size, dtype):
+    import ctypes
+    B, H, W, C, groups = size
+    d = make(B, H, W, C, dtype, seed=11)
+    y, stats = dcn.group_norm_forward(d["x"], d["ga"], d["be"], groups, EPS, "silu")
+    gx, gg, gb = dcn.group_norm_backward(d["x"], d["ga"], d["be"], stats, d["gy"], groups, "silu")
+    x = d["x"].clone()
+    dcn.group_norm_forward(x, d["ga"], d["be"], groups, EPS, "silu", out=x)
+    assert torch.equal(x, y)
+    p = dcn.NormParams(B, H, W, C, groups, EPS, dcn.ACTIVATIONS["silu"], int(dtype == "bf16"), 0)
+    ws = torch.empty(dcn.group_norm_workspace_size(p, dcn.OP_BACKWARD), dtype=torch.uint8, device="cuda")
+    gy, gg2, gb2 = d["gy"].clone(), torch.empty_like(gg), torch.empty_like(gb)
+    rc = dcn._load().dcn_group_norm_backward(
+        ctypes.byref(p), d["x"].data_ptr(), d["ga"].data_ptr(), d["be"].data_ptr(), stats.data_ptr(), gy.data_ptr(),
+        gy.data_ptr(), gg2.data_ptr(), gb2.data_ptr(), ws.data_ptr(), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    dcn.check_status()
+    assert torch.equal(gy, gx) and torch.equal(gg2, gg) and torch.equal(gb2, gb)
+
+
+def test_group_norm_refuses_overlaps():
+    buf = torch.zeros(2 * 8 * 8 * 16 + 16, device="cuda")
+    n = 2 * 8 * 8 * 16
+    x, y = buf[:n].view(2, 8, 8, 16), buf[16:].view(2, 8, 8, 16)
+    with pytest.raises(dcn.DcnError, match="overlaps"):
+        dcn.group_norm_forward(x, None, None, 4, out=y)

@@ -263,3 +263,13 @@ def test_linear_refusals_on_the_device():
         dcn.linear_backward(d["x"], d["w"], None, d["x"], "none")
     with pytest.raises(ValueError, match="CUDA"):
         dcn.linear_forward(d["x"], d["w"], d["b"].cpu())
+
+
+@pytest.mark.parametrize("M", [3, 64])
+def test_linear_refuses_overlaps(M):
+    x, w = torch.zeros(M, 64, device="cuda"), torch.zeros(64, 64, device="cuda")
+    with pytest.raises(dcn.DcnError, match="overlaps"):
+        dcn.linear_forward(x, w, out=x)
+    if M == 64:
+        with pytest.raises(dcn.DcnError, match="overlaps"):
+            dcn.linear_forward(x, w, out=w)

@@ -169,3 +169,53 @@ def test_workspace_sizes(lib):
     assert dcn.linear_workspace_size(LP(M=8, N=1024, K=12544), dcn.OP_FORWARD) == 0
     assert dcn.linear_workspace_size(LP(M=9, N=1024, K=12544), dcn.OP_FORWARD) <= 64 * 9 * 1024 * 4
     assert dcn.group_norm_workspace_size(NP(B=8, H=200, W=200, C=128, groups=32), dcn.OP_FORWARD) < 1 << 22
+
+
+def at(k, size=0):
+    """An address in a place of its own, far from the other places."""
+    return ctypes.c_void_p((k << 30) + size)
+
+
+@pytest.mark.parametrize("M", [5, 200])  # the few rows' kernel, tensor cores
+@pytest.mark.parametrize("out,of", [("y", "x"), ("y", "w"), ("y", "b"), ("z", "x"), ("z", "r"), ("z", "y"), ("ws", "x")])
+def test_linear_forward_refuses_overlaps(lib, M, out, of):
+    p = LP(M=M, N=64, K=64 if M == 5 or out != "ws" else 65)
+    if out == "ws" and lib.dcn_linear_workspace_size(ctypes.byref(p), 0) == 0:
+        pytest.skip("no workspace")
+    place = {k: at(i + 1) for i, k in enumerate(("x", "w", "b", "r", "y", "z", "ws"))}
+    assert M == 5 or lib.dcn_linear_workspace_size(ctypes.byref(p), 0) <= 1 << 30
+    place[out] = ctypes.c_void_p(place[of].value)
+    assert lin_fwd(lib, p, **place) == EINVAL
+    assert "overlaps" in lib.dcn_last_error_string().decode()
+
+
+def test_linear_forward_refuses_a_shifted_residual(lib):
+    p = LP(M=200, N=64, K=64)
+    assert lin_fwd(lib, p, at(1), at(2), at(3), at(4), at(4, 16), None) == EINVAL
+    assert lin_fwd(lib, p, at(1), at(2), at(3), at(4, 16), at(4), None) == EINVAL
+
+
+@pytest.mark.parametrize("out", ["gx", "gw", "gb", "gr", "ws"])
+@pytest.mark.parametrize("of", ["x", "w", "s", "gy"])
+def test_linear_backward_refuses_overlaps(lib, out, of):
+    p = LP(M=200, N=64, K=64)
+    place = {k: at(i + 1) for i, k in enumerate(("x", "w", "s", "gy", "gx", "gw", "gb", "gr", "ws"))}
+    place[out] = place[of]
+    assert lin_bwd(lib, p, **place) == EINVAL
+    place = {k: at(i + 1) for i, k in enumerate(("x", "w", "s", "gy", "gx", "gw", "gb", "gr", "ws"))}
+    place["gr"] = place["gx"]
+    assert lin_bwd(lib, p, **place) == EINVAL
+
+
+@pytest.mark.parametrize("side", [7, 333])
+def test_group_norm_refuses_overlaps(lib, side):
+    p = NP(B=2, H=side, W=side, C=64, groups=8)
+    fwd, bwd = lib.dcn_group_norm_forward, lib.dcn_group_norm_backward
+    q = ctypes.byref(p)
+    assert fwd(q, at(1), at(2), at(3), at(1, 16), at(5), at(6), BIG, None) == EINVAL
+    assert fwd(q, at(1), at(2), at(3), at(2), at(5), at(6), BIG, None) == EINVAL
+    assert fwd(q, at(1), at(2), at(3), at(4), at(1), at(6), BIG, None) == EINVAL
+    assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(1), at(7), at(8), at(9), BIG, None) == EINVAL
+    assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(5, 16), at(7), at(8), at(9), BIG, None) == EINVAL
+    assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(6), at(2), at(8), at(9), BIG, None) == EINVAL
+    assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(6), at(7), at(7), at(9), BIG, None) == EINVAL
