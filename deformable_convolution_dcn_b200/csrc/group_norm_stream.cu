@@ -7,7 +7,9 @@
 // of one stage, to a ring of shared-memory stages (bulk copies, up to 160 KB in
 // flight); most warps compute from there and store; four more warps count the summed
 // units and join their sets. So the memory works on while sums are counted, joined and
-// released, and those latencies cost little: with the fence and the atomic in a
+// released, and those latencies cost little (bfloat16: 8x200x200x128 silu 59 us,
+// 8x100x100x256 relu backward 69, both bound by the instructions of the computing warps,
+// 36 to 46 % of the issue slots with one block an SM, and by the waits between the passes): with the fence and the atomic in a
 // computing warp a unit cost nine microseconds more, in a kernel without the ring
 // (group_norm.cu) 8x200x200x128 takes 92 us. The producer waits for a set's statistics
 // before it copies a unit of the second pass, and leaves them in its first stage.
