@@ -8,11 +8,10 @@
 // Sums are float32 pairs (fma.f32x2), joined by a butterfly over the lanes and
 // then over the warps, in a fixed order.
 //
-// N x K of 1024 x 12544 bfloat16 (25.7 MB, 3.9 us at HBM rate): 5.8 us for one row,
-// 7.8 for two, 14.2 for five to eight, where x's loads and the sums bound it. The
-// tensor-core kernel, with its reduction split 18 times and a joining launch, takes
-// 13.3 us on the GPU, but a call 16.9 us where this one's is 14.6 (host time). float32:
-// 10.2 us for one row, 22.8 for eight, tensor cores 45.2.
+// N x K of 1024 x 12544 bfloat16 (25.7 MB, 3.9 us at HBM rate): 5.8 to 6.7 us for one
+// row, 8.2 for two, 10.9 for five, 12.8 for eight, where x's loads and the sums bound
+// it. The tensor-core kernel, with its reduction split 18 times and a joining launch,
+// takes 13.3 us. float32: 10.3 us for one row, 22.8 for eight, tensor cores 45.2.
 #include <algorithm>
 #include <type_traits>
 
@@ -50,7 +49,8 @@ template <typename T, int NR, int MB, int ACT>
 __global__ void __launch_bounds__(NT, MB > 2 ? 2 : 3)
     few_kernel(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const T* residual, T* y, T* z,
                int M, int N, int K, int team) {
-    constexpr int V = 16 / (int)sizeof(T), P = V / 2, NV = NR * MB, DEPTH = 8 / NR;
+    constexpr int V = 16 / (int)sizeof(T), P = V / 2, DEPTH = 8 / NR;
+    constexpr int MP = MB == 6 ? 8 : MB, NV = NR * MP;  // the butterfly wants a power of two
     __shared__ float sm[WARPS][NV];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -91,14 +91,14 @@ __global__ void __launch_bounds__(NT, MB > 2 ? 2 : 3)
                 }
             }
         }
-        float v[NV];
+        float v[NV] = {};
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
                 float lo, hi;
                 split(acc[r][m], lo, hi);
-                v[r * MB + m] = lo + hi;
+                v[r * MP + m] = lo + hi;
             }
         float sum = butterfly<NV>(v);
         if (team > 1) {
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NT, MB > 2 ? 2 : 3)
                 for (int k = 1; k < team; ++k) sum += sm[warp + k][lane];
             __syncthreads();  // sm is free
         }
-        const int n = n0 + lane / MB, m = lane % MB;
+        const int n = n0 + lane / MP, m = lane % MP;
         if (warp % team == 0 && lane < NV && n < N && m < M) {
             const size_t at = (size_t)m * N + n;
             if (bias) sum += ld1(bias + n);
@@ -123,9 +123,15 @@ template <typename T, int NR, int MB>
 cudaError_t run(const LinearShape& s, const T* x, const T* w, const T* bias, const T* residual, T* y, T* z,
                 cudaStream_t st) {
     return with_act(s.act, [&](auto A) {
+        // Warps that share a group: with many rows of x few, so that a block's teams read the same x from L1 (5 x 1024
+        // x 12544 bfloat16, eight warps 14.2 us, four 12.5), unless too few blocks are left (float32 5 x 2048 x 2048,
+        // one warp 10.1 us, two 7.0).
+        const int groups = (s.N + NR - 1) / NR, kv = s.K / (16 / (int)sizeof(T));
         int team = 1;
-        while (team < WARPS && s.K / (16 / (int)sizeof(T)) > team * (MB > 2 ? 256 : 64)) team *= 2;
-        const int groups = (s.N + NR - 1) / NR, teams = WARPS / team;
+        while (team < WARPS &&
+               (kv > team * (MB > 2 ? 512 : 64) || (kv > team * 256 && (long long)groups * team < WARPS * num_sms())))
+            team *= 2;
+        const int teams = WARPS / team;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)std::min((groups + teams - 1) / teams, num_sms() * (MB > 2 ? 2 : 3)));
         cfg.blockDim = dim3(NT);
@@ -155,16 +161,19 @@ cudaError_t forward_t(const LinearShape& s, const T* x, const T* w, const T* bia
     if (s.M == 1) return run_m<T, 1>(s, x, w, bias, residual, y, z, st);
     if (s.M == 2) return run_m<T, 2>(s, x, w, bias, residual, y, z, st);
     if (s.M <= 4) return run_m<T, 4>(s, x, w, bias, residual, y, z, st);
+    // (eight rows' kernel for five took 14.2 us where this one's 10.9 to 12)
+    if (s.M <= 6) return run_m<T, 6>(s, x, w, bias, residual, y, z, st);
     return run_m<T, 8>(s, x, w, bias, residual, y, z, st);
 }
 
 }  // namespace
 
-// Five rows and more of a large bfloat16 weight keep the tensor cores: 5 x 4096 x 4096 takes 16.8 us here and 13.3 us
-// there, 5 x 1024 x 12544 14.2 and 13.3 us (but in one launch), float32 5 x 4096 x 4096 26 and 56 us.
+// More rows of a large bfloat16 weight keep the tensor cores, whose time hardly grows with them: 5 x 4096 x 4096 takes
+// 13.0 us here and 12.6 there, 8 x 4096 x 4096 15.6 and 12.4, 4 x 2048 x 12544 16.1 and 16.9, 4 x 8192 x 4096 19.3 and
+// 18.4; but 5 x 1024 x 12544 10.9 and 13.3, 2 x 4096 x 4096 10.5 and 12.6. (float32 5 x 4096 x 4096 19 and 56 us.)
 bool linear_few_supported(const LinearShape& s, int bf) {
     if (s.M > 8 || s.K % (bf ? 8 : 4)) return false;
-    return !bf || s.M <= 4 || (long long)s.N * s.K < (1LL << 24);
+    return !bf || s.M <= 2 || (long long)s.N * s.K < (s.M <= 4 ? 1LL << 25 : 1LL << 24);
 }
 
 cudaError_t linear_few_forward(const LinearShape& s, int bf, const void* x, const void* w, const void* bias,
