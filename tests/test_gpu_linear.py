@@ -273,3 +273,25 @@ def test_linear_refuses_overlaps(M):
     if M == 64:
         with pytest.raises(dcn.DcnError, match="overlaps"):
             dcn.linear_forward(x, w, out=w)
+
+
+# one output a row (a one-channel 1x1 convolution): bfloat16 rows on the tensor cores' columns (the first three), and not
+@pytest.mark.parametrize("size", [(262144, 1, 512), (170519, 1, 1024), (19005, 1, 12544), (60000, 1, 2048), (4099, 1, 33)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+def test_linear_one_output(size, dtype, residual):
+    """The bias is one value, whatever lies behind it."""
+    M, N, K = size
+    g = torch.Generator(device="cuda").manual_seed(12)
+    n = lambda *s, k=1.0: (torch.randn(s, generator=g, device="cuda") * k).to(TYPES[dtype])  # noqa: E731
+    room = torch.full((M + 64,), float("nan"), dtype=TYPES[dtype], device="cuda")
+    room[0] = 0.75
+    x, w, r = n(M, K), n(1, K, k=K ** -0.5), n(M, 1) if residual else None
+    y = dcn.linear_forward(x, w, room[:1], r, "relu")
+    torch.cuda.synchronize()
+    dcn.check_status()
+    ref.check("y", y, *ref.linear_forward(x, w, room[:1], r, "relu")["y"])
+    if residual:
+        dcn.linear_forward(x, w, room[:1], r, "relu", out=r)
+        assert torch.equal(r, y)
