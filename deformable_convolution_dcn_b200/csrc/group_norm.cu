@@ -18,7 +18,8 @@
 //
 // A block claims its units by an atomic counter, in order. A unit of the second
 // pass waits for units ahead of it in the queue alone, so the lowest unfinished
-// unit can always run, however many blocks are resident. The waits are bounded.
+// unit can always run, however many blocks are resident. The waits are bounded; a
+// block whose wait ran out takes no more units, and the status word says so.
 //
 // A thread keeps one 16-byte vector of channels and walks the pixels, eight
 // loads in flight. Sums are float32: the statistics are taken about the unit's
@@ -38,7 +39,10 @@ namespace {
 constexpr int NT = 256;                 // threads a block
 constexpr int MAX_COLS = 1024;          // channels a unit at most (V = 1: 256)
 constexpr int UNIT_BYTES = 96 * 1024;   // of a map that fills the GPU many times
-constexpr long long WAIT_LIMIT = 2000000000LL;
+#ifndef DCN_NORM_WAIT_LIMIT  // cycles; a test's build sets fewer
+#define DCN_NORM_WAIT_LIMIT 2000000000LL
+#endif
+constexpr long long WAIT_LIMIT = DCN_NORM_WAIT_LIMIT;
 
 // How a map is cut. Blocks of cb channels: gpb whole groups, or (gpb = 0) parts
 // of one group.
@@ -204,15 +208,20 @@ __device__ __forceinline__ float2 ld_l2(const float2* p) {
 // unit is made a unit ahead, and whether a summed unit was its set's last is looked at a unit later.
 struct Queue {
     const Args& a;
-    int* shared;          // [2]: the unit claimed, the set to join (or -1)
+    int* shared;          // [3]: the unit claimed, the set to join (or -1), whether a wait ran out
     int total;
     int claim = 0;        // thread 0
     int count = 0;        // thread 0: units summed of `set` before the last one summed here
     int set = -1;         // the set of the unit summed last, until that is looked at
     __device__ Queue(const Args& args, int* s) : a(args), shared(s) {
         total = 2 * a.s.B * a.p.sets * a.p.units;
-        if (threadIdx.x == 0) claim = atomicAdd(a.ticket, 1);
+        if (threadIdx.x == 0) {
+            shared[2] = 0;
+            claim = atomicAdd(a.ticket, 1);
+        }
     }
+    // A wait ran out (any thread): the next unit is none, so that the block ends instead of waiting again for each.
+    __device__ void stop() { shared[2] = 1; }
     // The next unit (total or more: none is left), and the set that this block has to join, or -1. All threads; the
     // barriers also free the unit's shared memory.
     __device__ int next(int& join) {
@@ -221,7 +230,7 @@ struct Queue {
             shared[1] = set >= 0 && count == a.p.units - 1 ? set : -1;
         }
         __syncthreads();
-        const int t = shared[0];
+        const int t = shared[2] ? total : shared[0];
         join = shared[1];
         set = -1;
         __syncthreads();
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(NT, 3)
                    T* __restrict__ y, float* __restrict__ stats) {
     __shared__ float sm[2 * NT * V];  // [2][ty][cb] sums, reused as [2][cb]
     __shared__ float first[NT * V];   // the unit's first pixel, [cb]
-    __shared__ int shared[2];
+    __shared__ int shared[3];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const NormShape& s = a.s;
@@ -423,7 +432,11 @@ __global__ void __launch_bounds__(NT, 3)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) q[j] = ptx::ldg_v4_stream(xp + (size_t)(r + j * ty) * s.C);
             }
-            if (!await_set(a, set) || !in) continue;
+            if (!await_set(a, set)) {
+                queue.stop();
+                continue;
+            }
+            if (!in) continue;
             float m[V], sc[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(NT, 2)
                     const float* __restrict__ stats, const T* __restrict__ gy, T* __restrict__ gx,
                     float* __restrict__ gg, float* __restrict__ gb) {
     __shared__ float sm[2 * NT * V];  // [2][ty][cb]
-    __shared__ int shared[2], flag;
+    __shared__ int shared[3], flag;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const NormShape& s = a.s;
@@ -631,7 +644,11 @@ __global__ void __launch_bounds__(NT, 2)
             }
             queue.summed(set);
         } else {
-            if (!await_set(a, set) || !in) continue;
+            if (!await_set(a, set)) {
+                queue.stop();
+                continue;
+            }
+            if (!in) continue;
             float c1[V], c2[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {

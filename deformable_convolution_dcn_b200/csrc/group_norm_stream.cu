@@ -15,7 +15,8 @@
 // before it copies a unit of the second pass, and leaves them in its first stage.
 //
 // A claimed unit waits for none but lower ones, which are summed by blocks that
-// never wait (see group_norm.cu), and the warps that join wait for no unit.
+// never wait (see group_norm.cu), and the warps that join wait for no unit. Every wait
+// is bounded; when one runs out, the block's warps leave and the status word says so.
 #include <algorithm>
 #include <type_traits>
 
@@ -35,7 +36,10 @@ constexpr int MAX_C = 1024;
 constexpr int MAX_GROUPS = 256;          // their statistics travel in a stage
 constexpr uint32_t RING = 168 * 1024;    // all stages
 constexpr uint32_t RED_BYTES = 2 * NC_FWD * 8 * 4;
-constexpr long long WAIT_LIMIT = 2000000000LL;
+#ifndef DCN_NORM_WAIT_LIMIT  // cycles; a test's build sets fewer
+#define DCN_NORM_WAIT_LIMIT 2000000000LL
+#endif
+constexpr long long WAIT_LIMIT = DCN_NORM_WAIT_LIMIT;
 
 struct StreamPlan {
     bool ok;
@@ -114,11 +118,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-template <int NC>
-__device__ __forceinline__ void sync_computing() {
-    ptx::bar_sync_named(1, NC);
-}
-
 // Waits, a warp, until the set's sums are joined; false when the bounded wait ran out.
 __device__ __forceinline__ bool await_set(const Args& a, int set) {
     bool ok = true;
@@ -143,6 +142,27 @@ struct Ring {
     // summed units on their way to the joining warps, in two slots: the set (-1: no more), its barriers
     int* unit_set;
     uint32_t unit_done, unit_free;
+    volatile int* aborted;  // a wait of the block ran out: every warp leaves
+};
+
+// A barrier of some of the block's warps that none is left waiting at. After a wait that ran out warps leave one by one;
+// each arrives once more as it leaves, at the barrier that the others may be waiting at. They find `aborted` set behind
+// it, which the first to leave had set before it arrived, and leave too. (Barriers with bounded waits of their own,
+// mbarriers, took 62.5 us where this takes 59.8, 8x200x200x128.)
+struct Meet {
+    int id, threads;
+    volatile int* aborted;
+    // All lanes; false: leave.
+    __device__ __forceinline__ bool operator()() const {
+        ptx::bar_sync_named(id, threads);
+        return !__any_sync(~0u, *aborted) || leave();
+    }
+    __device__ __forceinline__ bool leave() const {
+        __threadfence_block();
+        __syncwarp();
+        ptx::bar_arrive_named(id, threads);
+        return false;
+    }
 };
 
 // The producer warp. MAPS: x, or x and grad_y; stats: the backward's (mean, rstd); apply: the second pass is wanted.
@@ -154,9 +174,8 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
     const int lane = threadIdx.x % 32;
     const int total = (apply ? 2 : 1) * s.B * p.chunks;
     const uint32_t row = s.C * (uint32_t)sizeof(T);
-    int stage = 0;
+    int stage = 0, copied = 0;
     uint32_t phase = 1;
-    volatile int none = 0;
     bool ok = true;
     // Claimed when the unit before is on its way, not earlier: the ring hides the answer's time, and a unit held by a
     // block that is not at it is one that an idle block misses.
@@ -173,7 +192,7 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
         }
         for (int k = chunk; k < p.blocks; k += p.chunks) {
             const int r = k * p.srows;
-            ok = __all_sync(~0u, ptx::mbar_wait(ring.empty + stage * 8, phase, &none, a.status, WAIT_LIMIT));
+            ok = __all_sync(~0u, ptx::mbar_wait(ring.empty + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT));
             if (!ok) break;
             const int n = min(p.srows, s.HW - r);
             if (k == chunk) {  // the statistics that the unit needs
@@ -198,18 +217,27 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
                 if (MAPS == 2) ptx::bulk_load(dst + p.data, gy + at, bytes, bar);
             }
             __syncwarp();
+            ++copied;
             if (++stage == p.stages) stage = 0, phase ^= 1;
         }
     }
     // the end, in a stage of its own
-    ptx::mbar_wait(ring.empty + stage * 8, phase, &none, a.status, WAIT_LIMIT);
+    ok = __all_sync(~0u, ptx::mbar_wait(ring.empty + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT));
     if (lane == 0) {
-        ring.headers[stage].pass = -1;
-        ptx::mbar_arrive(ring.full + stage * 8);
+        if (ok) {
+            ring.headers[stage].pass = -1;
+            ptx::mbar_arrive(ring.full + stage * 8);
+        }
+        // copies still in flight land before the block may end (that of the end's stage has: the stage was free)
+        volatile int none = 0;
+        for (int k = max(0, copied - p.stages + (ok ? 1 : 0)); k < copied; ++k)
+            ptx::mbar_wait(ring.full + (k % p.stages) * 8, (k / p.stages) & 1, &none, nullptr, WAIT_LIMIT);
     }
+    __syncwarp();
 }
 
-__device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t* bars, int* unit_set, int warps) {
+__device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t* bars, int* unit_set, int* aborted,
+                                        int warps) {
     Ring r;
     r.smem = smem;
     r.base = ptx::smem_u32(smem);
@@ -219,7 +247,9 @@ __device__ __forceinline__ Ring ring_of(uint8_t* smem, Header* headers, uint64_t
     r.unit_set = unit_set;
     r.unit_done = r.empty + MAX_STAGES * 8;
     r.unit_free = r.unit_done + 16;
+    r.aborted = aborted;
     if (threadIdx.x == 0) {
+        *aborted = 0;
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(r.unit_done + i * 8, warps);
             ptx::mbar_init(r.unit_free + i * 8, 1);
@@ -263,9 +293,8 @@ struct Post {
     // The unit's pieces are written by this thread; set -1: no more units. All computing threads.
     __device__ __forceinline__ void operator()(const Args& a, const Ring& ring, int set) {
         const int slot = n & 1;
-        volatile int none = 0;
         if (threadIdx.x == 0) {  // the slot's unit before the last has been taken
-            if (n >= 2) ptx::mbar_wait(ring.unit_free + slot * 8, ((n >> 1) - 1) & 1, &none, a.status, WAIT_LIMIT);
+            if (n >= 2) ptx::mbar_wait(ring.unit_free + slot * 8, ((n >> 1) - 1) & 1, ring.aborted, a.status, WAIT_LIMIT);
             ring.unit_set[slot] = set;
         }
         __syncwarp();
@@ -274,30 +303,32 @@ struct Post {
     }
 };
 
-__device__ __forceinline__ void sync_joiners() { ptx::bar_sync_named(2, JOINERS); }
-
-// The joining warps: counts each summed unit in its set, and join(set) for the sets that this block has finished.
+// The joining warps: counts each summed unit in its set, and join(set, meet) for the sets that this block has finished
+// (false: leave).
 template <typename F>
 __device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* flag, F&& join) {
     const bool head = threadIdx.x % 32 == 0 && (int)threadIdx.x == (int)blockDim.x - JOINERS;
-    volatile int none = 0;
+    const Meet meet{2, JOINERS, ring.aborted};
     for (int n = 0;; ++n) {
         const int slot = n & 1;
-        // a unit may be a long time away (the wait of the producer among the reasons): no limit but the kernel's own end
-        if (!ptx::mbar_wait(ring.unit_done + slot * 8, (n >> 1) & 1, &none, a.status, 4 * WAIT_LIMIT)) return;
+        // a unit may be a long time away, the wait of the producer among the reasons
+        const bool ok = ptx::mbar_wait(ring.unit_done + slot * 8, (n >> 1) & 1, ring.aborted, a.status, 4 * WAIT_LIMIT);
+        if (!__all_sync(~0u, ok)) {
+            meet.leave();
+            return;
+        }
         const int set = ring.unit_set[slot];
         if (set < 0) return;
-        sync_joiners();
+        if (!meet()) return;
         if (head) {
             ptx::mbar_arrive(ring.unit_free + slot * 8);
             __threadfence();
             *flag = atomicAdd(a.done + set, 1) == a.p.chunks - 1;
             __threadfence();
         }
-        sync_joiners();
+        if (!meet()) return;
         if (*flag) {
-            join(set);
-            sync_joiners();  // all of it is written
+            if (!join(set, meet) || !meet()) return;  // all of it is written
             if (head) {
                 __threadfence();
                 atomicExch(a.ready + set, 1);
@@ -308,7 +339,7 @@ __device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* 
 
 // The forward's join: mean and rstd of a set's groups. Four threads share a group's units; sums are taken about the
 // first unit's mean.
-__device__ __forceinline__ void join_stats(const Args& a, int set, float* stats, float4* sm) {
+__device__ __forceinline__ bool join_stats(const Args& a, const Meet& meet, int set, float* stats, float4* sm) {
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     const int t = threadIdx.x - (blockDim.x - JOINERS), cg = s.C / s.groups;
@@ -329,7 +360,7 @@ __device__ __forceinline__ void join_stats(const Args& a, int set, float* stats,
             }
         }
         sm[t] = make_float4(u, sq, m2, 0.f);
-        sync_joiners();
+        if (!meet()) return false;
         if (part == 0 && g < s.groups) {
             for (int k = 1; k < JOINERS / 32; ++k) {
                 const float4 v = sm[k * 32 + t];
@@ -346,8 +377,9 @@ __device__ __forceinline__ void join_stats(const Args& a, int set, float* stats,
                 stats[2 * o + 1] = v.y;
             }
         }
-        sync_joiners();
+        if (!meet()) return false;
     }
+    return true;
 }
 
 template <typename T, int ACT>
@@ -357,13 +389,13 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_FWD, WARPS = NC / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[2 * MAX_STAGES + 4];
-    __shared__ int unit_set[2];
+    __shared__ int unit_set[2], aborted;
     __shared__ Header headers[MAX_STAGES];
     __shared__ int flag;
     __shared__ float4 scratch[JOINERS];
-    const Ring ring = ring_of(smem, headers, bars, unit_set, NC / 32);
+    const Ring ring = ring_of(smem, headers, bars, unit_set, &aborted, NC / 32);
     if (threadIdx.x >= NC + 32) {
-        join_sets(a, ring, &flag, [&](int set) { join_stats(a, set, stats, scratch); });
+        join_sets(a, ring, &flag, [&](int set, const Meet& meet) { return join_stats(a, meet, set, stats, scratch); });
         return;
     }
     if (threadIdx.x >= NC) {
@@ -379,16 +411,20 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     // each channel's group (a division each, otherwise, for every unit)
     uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
     for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
-    sync_computing<NC>();
+    const Meet meet{1, NC, ring.aborted};
+    if (!meet()) return;
     // k: minus the unit's first pixel, or minus the mean; u, d: the sums, or rstd gamma and beta
     F2 k[P] = {}, u[P] = {}, d[P] = {};
     float* first = red + 2 * NC * V;  // [C] the unit's first pixel
     Post post;
-    volatile int none = 0;
     int stage = 0;
     uint32_t phase = 0;
     for (;;) {
-        if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
+        const bool there = ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT);
+        if (!__all_sync(~0u, there)) {
+            meet.leave();
+            return;
+        }
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
         const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
@@ -445,7 +481,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
-            sync_computing<NC>();
+            if (!meet()) return;
             const float count = (float)pixels_of(a, hd.chunk);
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
@@ -458,7 +494,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
                 red[c] = first[c] + m;
                 red[slots * s.C + c] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
             }
-            sync_computing<NC>();
+            if (!meet()) return;
             for (int g = warp; g < s.groups; g += WARPS) {
                 float e = 0.f;
                 for (int c = lane; c < cg; c += 32) e += red[g * cg + c];
@@ -473,7 +509,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
                     a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.groups + g] = make_float2(mean, m2);
             }
             post(a, ring, hd.set);
-            sync_computing<NC>();  // red is free
+            if (!meet()) return;  // red is free
         }
     }
     post(a, ring, -1);
@@ -482,8 +518,8 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
 // The backward's join: the sums of a set's channels, c1 and c2 of its groups; after the last set of all, the
 // parameters' gradients. sm: [2][MAX_C].
 template <typename T>
-__device__ __forceinline__ void join_sums(const Args& a, int set, const T* gamma, float* gg, float* gb, float* sm,
-                                          int* last) {
+__device__ __forceinline__ bool join_sums(const Args& a, const Meet& meet, int set, const T* gamma, float* gg,
+                                          float* gb, float* sm, int* last) {
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     const int t = threadIdx.x - (blockDim.x - JOINERS), warp = t / 32, lane = t % 32, cg = s.C / s.groups;
@@ -502,7 +538,7 @@ __device__ __forceinline__ void join_sums(const Args& a, int set, const T* gamma
         sm[c] = k * v.x;
         sm[MAX_C + c] = k * v.y;
     }
-    sync_joiners();
+    if (!meet()) return false;
     const float inv = 1.f / ((float)s.HW * (float)cg);
     for (int g = warp; g < s.groups; g += JOINERS / 32) {
         float e = 0.f, f = 0.f;
@@ -515,16 +551,17 @@ __device__ __forceinline__ void join_sums(const Args& a, int set, const T* gamma
         if (lane == 0) c12[(size_t)set * s.groups + g] = make_float2(e * inv, f * inv);
     }
     if (gg || gb) {
-        sync_joiners();
+        if (!meet()) return false;
         if (t == 0) {
             __threadfence();
             *last = atomicAdd(a.finished, 1) == s.B - 1;
             __threadfence();
         }
-        sync_joiners();
+        if (!meet()) return false;
         if (*last)
             for (int c = t; c < s.C; c += JOINERS) params_of(s, csums, c, gg, gb);
     }
+    return true;
 }
 
 template <typename T, int ACT>
@@ -535,13 +572,15 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     constexpr int V = 16 / (int)sizeof(T), P = V / 2, NC = NC_BWD;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[2 * MAX_STAGES + 4];
-    __shared__ int unit_set[2];
+    __shared__ int unit_set[2], aborted;
     __shared__ Header headers[MAX_STAGES];
     __shared__ int flag, last;
     __shared__ float scratch[2 * MAX_C];
-    const Ring ring = ring_of(smem, headers, bars, unit_set, NC / 32);
+    const Ring ring = ring_of(smem, headers, bars, unit_set, &aborted, NC / 32);
     if (threadIdx.x >= NC + 32) {
-        join_sets(a, ring, &flag, [&](int set) { join_sums(a, set, gamma, gg, gb, scratch, &last); });
+        join_sets(a, ring, &flag, [&](int set, const Meet& meet) {
+            return join_sums(a, meet, set, gamma, gg, gb, scratch, &last);
+        });
         return;
     }
     if (threadIdx.x >= NC) {
@@ -557,7 +596,8 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     // each channel's group (a division each, otherwise, for every unit)
     uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
     for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
-    sync_computing<NC>();
+    const Meet meet{1, NC, ring.aborted};
+    if (!meet()) return;
     Post post;
     Channels<P> ch = {};
     F2 u[P] = {}, d[P] = {};  // the sums, or -c1 and -c2
@@ -568,11 +608,14 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
         ch.be[i] = f2(beta ? ld1(beta + c) : 0.f, beta ? ld1(beta + c + 1) : 0.f);
     }
     ch.set_border();
-    volatile int none = 0;
     int stage = 0;
     uint32_t phase = 0;
     for (;;) {
-        if (!ptx::mbar_wait(ring.full + stage * 8, phase, &none, a.status, WAIT_LIMIT)) break;
+        const bool there = ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT);
+        if (!__all_sync(~0u, there)) {
+            meet.leave();
+            return;
+        }
         const Header hd = headers[stage];
         if (hd.pass < 0) break;
         const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
@@ -628,7 +671,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
-            sync_computing<NC>();
+            if (!meet()) return;
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
 #pragma unroll 8
@@ -639,7 +682,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
                 a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.C + c] = make_float2(e, f);
             }
             post(a, ring, hd.set);
-            sync_computing<NC>();  // red is free
+            if (!meet()) return;  // red is free
         }
     }
     post(a, ring, -1);

@@ -219,3 +219,17 @@ def test_group_norm_refuses_overlaps(lib, side):
     assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(5, 16), at(7), at(8), at(9), BIG, None) == EINVAL
     assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(6), at(2), at(8), at(9), BIG, None) == EINVAL
     assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(6), at(7), at(7), at(9), BIG, None) == EINVAL
+
+
+def test_norm_barriers_hold_no_warp_that_others_left():
+    """In the kernel whose warps wait by themselves, hardware barriers stand in Meet alone (a warp that leaves early
+    arrives there for the others), and no way out of a failed wait goes past it."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(dcn.__file__), "csrc", "group_norm_stream.cu")).read()
+    meet = src[src.index("struct Meet {"):src.index("// The producer warp")]
+    rest = src.replace(meet, "")
+    assert "bar_sync" not in rest and "bar.sync" not in rest and "bar_arrive" not in rest
+    assert meet.count("bar_sync_named") == 1 and meet.count("bar_arrive_named") == 1
+    assert "&none" not in re.sub(r"volatile int none = 0;\n\s+for .*\n.*&none, nullptr.*", "", rest)
+    assert len(re.findall(r"if \(!__all_sync\(~0u, (?:there|ok)\)\) \{\n\s+meet\.leave\(\);\n\s+return;", rest)) == 3
