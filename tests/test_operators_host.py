@@ -229,7 +229,7 @@ def test_norm_barriers_hold_no_warp_that_others_left():
     src = open(os.path.join(os.path.dirname(dcn.__file__), "csrc", "group_norm_stream.cu")).read()
     meet = src[src.index("struct Meet {"):src.index("// The producer warp")]
     rest = src.replace(meet, "")
-    assert "bar_sync" not in rest and "bar.sync" not in rest and "bar_arrive" not in rest
+    assert "bar_sync_named" not in rest and "bar.sync" not in rest and "bar_arrive_named" not in rest
     assert meet.count("bar_sync_named") == 1 and meet.count("bar_arrive_named") == 1
     assert "&none" not in re.sub(r"volatile int none = 0;\n\s+for .*\n.*&none, nullptr.*", "", rest)
     assert len(re.findall(r"if \(!__all_sync\(~0u, (?:there|ok)\)\) \{\n\s+meet\.leave\(\);\n\s+return;", rest)) == 3
