@@ -22,9 +22,10 @@
 // block whose wait ran out takes no more units, and the status word says so.
 //
 // A thread keeps one 16-byte vector of channels and walks the pixels, eight
-// loads in flight. Sums are float32: the statistics are taken about the unit's
-// first pixel and joined as means and sums of squares about them, so that a
-// level far from zero costs no digits.
+// loads in flight. Sums are float32: the statistics are taken about a level that
+// follows the mean (Running in norm.cuh) and joined as means and sums of squares
+// about them, so that a level far from zero costs no digits, nor does a first pixel
+// far from the others.
 #include <algorithm>
 #include <type_traits>
 
@@ -321,7 +322,6 @@ __global__ void __launch_bounds__(NT, 3)
     forward_kernel(const Args a, const T* __restrict__ x, const T* __restrict__ gamma, const T* __restrict__ beta,
                    T* __restrict__ y, float* __restrict__ stats) {
     __shared__ float sm[2 * NT * V];  // [2][ty][cb] sums, reused as [2][cb]
-    __shared__ float first[NT * V];   // the unit's first pixel, [cb]
     __shared__ int shared[3];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -344,9 +344,12 @@ __global__ void __launch_bounds__(NT, 3)
         const size_t at = (size_t)c.b * s.HW * s.C + c.c0 + cx * V;
         const T* xp = x + at;
         if (pass == 0) {
+            const int rows = c.r1 - c.r0;
             if (in) {
+                // see Running: k the level, s1 and s2 the sums about it
                 float k[V], s1[V] = {}, s2[V] = {};
-                load<T, V>(k, xp + (size_t)c.r0 * s.C);
+                int n = 0, next = 8;
+                load<T, V>(k, xp + (size_t)min(c.r0 + ry, c.r1 - 1) * s.C);
                 auto add = [&](const float(&v)[V]) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
@@ -355,46 +358,56 @@ __global__ void __launch_bounds__(NT, 3)
                         s2[i] = fmaf(d, d, s2[i]);
                     }
                 };
+                auto level = [&]() {
+                    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float m = s1[i] * inv;
+                        s2[i] = fmaf(-s1[i], m, s2[i]);
+                        k[i] += m;
+                        s1[i] = 0.f;
+                    }
+                };
                 int r = c.r0 + ry;
-                if constexpr (V > 1) {
-                    for (; r + 7 * ty < c.r1; r += 8 * ty) {
-                        uint4 q[8];
+                for (; r + 7 * ty < c.r1; r += 8 * ty) {
+                    typename std::conditional<V == 1, float, uint4>::type q[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) q[j] = ptx::ldg_v4_stream(xp + (size_t)(r + j * ty) * s.C);
+                    for (int j = 0; j < 8; ++j) {
+                        const T* at = xp + (size_t)(r + j * ty) * s.C;
+                        if constexpr (V > 1) q[j] = ptx::ldg_v4_stream(at);
+                        else q[j] = ld1(at);
+                    }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float v[V];
-                            unpack(v, q[j]);
-                            add(v);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        float v[V];
+                        if constexpr (V > 1) unpack(v, q[j]);
+                        else v[0] = q[j];
+                        add(v);
+                    }
+                    n += 8;
+                    if (n == next) {
+                        level();
+                        next *= 2;
                     }
                 }
 #pragma unroll 4
-                for (; r < c.r1; r += ty) {
+                for (; r < c.r1; r += ty, ++n) {
                     float v[V];
                     load<T, V>(v, xp + (size_t)r * s.C);
                     add(v);
                 }
+                level();
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sm[ry * p.cb + cx * V + i] = s1[i];
+                    sm[ry * p.cb + cx * V + i] = k[i];
                     sm[(ty + ry) * p.cb + cx * V + i] = s2[i];
-                    if (ry == 0) first[cx * V + i] = k[i];
                 }
             }
             __syncthreads();
-            const float n = (float)(c.r1 - c.r0);
-            for (int q = threadIdx.x; q < c.nc; q += NT) {
-                float u = 0.f, d = 0.f;
-#pragma unroll 8
-                for (int r = 0; r < ty; ++r) {
-                    u += sm[r * p.cb + q];
-                    d += sm[(ty + r) * p.cb + q];
-                }
-                const float m = u / n, m2 = d - u * m;  // about the first pixel
-                sm[q] = first[q] + m;
-                sm[ty * p.cb + q] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
-            }
+            const float n = (float)rows;
+            const int each = rows / ty, more = rows % ty;
+            for (int q = threadIdx.x; q < c.nc; q += NT)
+                join_slots(sm + q, p.cb, ty, n, [&](int r) { return (float)(each + (r < more)); });
             __syncthreads();
             // a warp joins the channels of a group: all have n values
             const int cw = p.gpb ? cg : c.nc;

@@ -107,9 +107,8 @@ __device__ __forceinline__ void unit_at(const Args& a, int t, int& pass, int& se
 
 // Pixels of a set's unit i.
 __device__ __forceinline__ int pixels_of(const Args& a, int i) {
-    const int runs = (a.p.blocks - 1 - i) / a.p.chunks + 1;
-    const bool last = (a.p.blocks - 1) % a.p.chunks == i;
-    return runs * a.p.srows - (last ? a.p.blocks * a.p.srows - a.s.HW : 0);
+    const int more = (a.p.blocks - 1) / a.p.chunks, last = a.p.blocks - 1 - more * a.p.chunks;
+    return (more + (i <= last)) * a.p.srows - (i == last ? a.p.blocks * a.p.srows - a.s.HW : 0);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -287,6 +286,38 @@ __device__ __forceinline__ int spread(F2 (&u)[P], F2 (&d)[P], int tx, int ty, in
     return slots;
 }
 
+// As spread, of moments: minus the levels (means) k, the squares about them d and the number of values n of each thread,
+// to red[2][slots][C] and counts[slots].
+template <int P, int NC>
+__device__ __forceinline__ int spread_moments(F2 (&k)[P], F2 (&d)[P], int n, int tx, int ty, int cx, int ry, int C,
+                                              float* red, float* counts) {
+    const bool pow2 = (tx & (tx - 1)) == 0 && tx < 32;
+    if (pow2)
+        for (int o = tx; o < 32; o <<= 1) {
+            const int nb = __shfl_xor_sync(~0u, n, o);
+            // the parts' weights: the mean moves by e nb / (n + nb), the squares grow by e^2 n nb / (n + nb)
+            const float w = (float)nb * rcp_fast((float)max(n + nb, 1));  // (a division took 1.5 us of 8x200x200x128)
+            const F2 wb = f2(w), wq = f2((float)n * w);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const F2 e = shfl_xor(k[i], o) + k[i] * f2(-1.f);
+                d[i] = fma(e * e, wq, d[i] + shfl_xor(d[i], o));
+                k[i] = fma(e, wb, k[i]);
+            }
+            n += nb;
+        }
+    const int slot = pow2 ? (int)threadIdx.x / 32 : ry, slots = pow2 ? NC / 32 : ty;
+    if (pow2 ? (int)(threadIdx.x % 32) < tx : ry < ty) {
+        if (cx == 0) counts[slot] = (float)n;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            *reinterpret_cast<F2*>(&red[slot * C + (cx * P + i) * 2]) = k[i] * f2(-1.f);
+            *reinterpret_cast<F2*>(&red[(slots + slot) * C + (cx * P + i) * 2]) = d[i];
+        }
+    }
+    return slots;
+}
+
 // The computing warps' side of the way to the joining warps.
 struct Post {
     int n = 0;
@@ -337,44 +368,64 @@ __device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* 
     }
 }
 
-// The forward's join: mean and rstd of a set's groups. Four threads share a group's units; sums are taken about the
-// first unit's mean.
+// The forward's join: mean and rstd of a set's groups. Four threads share a group's units, each with sums about a level
+// that moves to the mean after every batch of them (see Running).
 __device__ __forceinline__ bool join_stats(const Args& a, const Meet& meet, int set, float* stats, float4* sm) {
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     const int t = threadIdx.x - (blockDim.x - JOINERS), cg = s.C / s.groups;
-    const float total = (float)s.HW * (float)cg;
+    const float inv = 1.f / ((float)s.HW * (float)cg);
+    // values of a group in the units before, at and behind the one with the last run
+    const int most = (p.blocks - 1) / p.chunks, last = p.blocks - 1 - most * p.chunks;
+    const float before = (float)((most + 1) * p.srows) * (float)cg, behind = (float)(most * p.srows) * (float)cg;
+    const float at = (float)pixels_of(a, last) * (float)cg;
     for (int base = 0; base < s.groups; base += 32) {
         const int g = base + t % 32, part = t / 32;
-        float u = 0.f, sq = 0.f, m2 = 0.f, first = 0.f;
-        if (g < s.groups) {
+        float u = 0.f, m2 = 0.f, n = 0.f, level = 0.f;
+        if (g < s.groups && part < p.chunks) {
             const float2* pc = a.pieces + (size_t)set * p.chunks * s.groups + g;
-            first = __ldcg(pc).x;
-#pragma unroll 8
-            for (int i = part; i < p.chunks; i += JOINERS / 32) {
-                const float2 v = __ldcg(pc + (size_t)i * s.groups);
-                const float n = (float)pixels_of(a, i) * (float)cg, d = v.x - first;
-                u = fmaf(n, d, u);
-                sq = fmaf(n * d, d, sq);
-                m2 += v.y;
+            constexpr int STEP = JOINERS / 32, BATCH = 10;  // (units of a batch of eight samples: 18, 5 a thread)
+            for (int i0 = part; i0 < p.chunks; i0 += BATCH * STEP) {
+                float2 v[BATCH];  // all loads in flight
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+                    if (i0 + j * STEP < p.chunks) v[j] = __ldcg(pc + (size_t)(i0 + j * STEP) * s.groups);
+                if (i0 == part) level = v[0].x;
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+                    if (i0 + j * STEP < p.chunks) {
+                        const int i = i0 + j * STEP;
+                        const float c = i < last ? before : i == last ? at : behind, d = v[j].x - level;
+                        n += c;
+                        u = fmaf(c, d, u);
+                        m2 += fmaf(c * d, d, v[j].y);
+                    }
+                const float m = u * rcp_fast(n);
+                m2 = fmaf(-u, m, m2);
+                level += m;
+                u = 0.f;
             }
         }
-        sm[t] = make_float4(u, sq, m2, 0.f);
+        sm[t] = make_float4(n, level, m2, 0.f);
         if (!meet()) return false;
         if (part == 0 && g < s.groups) {
-            for (int k = 1; k < JOINERS / 32; ++k) {
-                const float4 v = sm[k * 32 + t];
-                u += v.x;
-                sq += v.y;
-                m2 += v.z;
+            float4 v[JOINERS / 32];
+            float e = 0.f, var = 0.f;
+#pragma unroll
+            for (int k = 0; k < JOINERS / 32; ++k) {
+                v[k] = sm[k * 32 + t];
+                if (v[k].x > 0.f) e = fmaf(v[k].x * inv, v[k].y - level, e);
             }
-            const float d = u / total, var = (m2 + (sq - u * d)) / total;
-            const float2 v = make_float2(first + d, rsqrtf((var < 0.f ? 0.f : var) + s.eps));
+            level += e;
+#pragma unroll
+            for (int k = 0; k < JOINERS / 32; ++k)
+                if (v[k].x > 0.f) var += fmaf(v[k].x * (v[k].y - level), v[k].y - level, v[k].z) * inv;
+            const float2 out = make_float2(level, rsqrtf((var < 0.f ? 0.f : var) + s.eps));
             const size_t o = (size_t)set * s.groups + g;
-            a.sets[o] = v;
+            a.sets[o] = out;
             if (stats) {
-                stats[2 * o] = v.x;
-                stats[2 * o + 1] = v.y;
+                stats[2 * o] = out.x;
+                stats[2 * o + 1] = out.y;
             }
         }
         if (!meet()) return false;
@@ -413,9 +464,12 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
     const Meet meet{1, NC, ring.aborted};
     if (!meet()) return;
-    // k: minus the unit's first pixel, or minus the mean; u, d: the sums, or rstd gamma and beta
-    F2 k[P] = {}, u[P] = {}, d[P] = {};
-    float* first = red + 2 * NC * V;  // [C] the unit's first pixel
+    // summing: see Running; applying: k minus the mean, u rstd gamma, d beta
+    Running<P> m = {};
+    auto &k = m.k, &u = m.u, &d = m.d;
+    int stages = 0, next = 1;         // of the unit, and at which the level moves
+    const int each = in && ry < p.srows ? (p.srows - 1 - ry) / ty + 1 : 0;  // this thread's pixels of a whole stage
+    float* counts = red + 2 * NC * V;  // [slots] values of a slot
     Post post;
     int stage = 0;
     uint32_t phase = 0;
@@ -432,26 +486,18 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
         if (!apply) {
             if (first_stage) {
-                unpack(k, q[0]);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (ry == 0) *reinterpret_cast<F2*>(&first[(cx * P + i) * 2]) = k[i];
-                    k[i] = k[i] * f2(-1.f);
-                    u[i] = d[i] = f2(0.f);
-                }
+                m.start(q[min(ry, n - 1) * tx]);
+                stages = 0;
+                next = 1;
             }
             if (in)
 #pragma unroll 4
-                for (int r = ry; r < n; r += ty) {
-                    F2 v[P];
-                    unpack(v, q[r * tx]);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const F2 e = v[i] + k[i];
-                        u[i] = u[i] + e;
-                        d[i] = fma(e, e, d[i]);
-                    }
-                }
+                for (int r = ry; r < n; r += ty) m.add(q[r * tx]);
+            if (++stages == next || last_stage) {  // (the stages before a unit's last are whole)
+                m.n = (stages - 1) * each + (n == p.srows ? each : in && ry < n ? (n - 1 - ry) / ty + 1 : 0);
+                m.level();
+                next *= 2;
+            }
         } else {
             if (first_stage) {
                 const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + p.data);
@@ -480,20 +526,11 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
-            const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
+            const int slots = spread_moments<P, NC>(k, d, m.n, tx, ty, cx, ry, s.C, red, counts);
             if (!meet()) return;
             const float count = (float)pixels_of(a, hd.chunk);
-            for (int c = threadIdx.x; c < s.C; c += NC) {
-                float e = 0.f, f = 0.f;
-#pragma unroll 8
-                for (int r = 0; r < slots; ++r) {
-                    e += red[r * s.C + c];
-                    f += red[(slots + r) * s.C + c];
-                }
-                const float m = e / count, m2 = f - e * m;  // about the first pixel
-                red[c] = first[c] + m;
-                red[slots * s.C + c] = m2 < 0.f ? 0.f : m2;  // a NaN stays one
-            }
+            for (int c = threadIdx.x; c < s.C; c += NC)
+                join_slots(red + c, s.C, slots, count, [&](int r) { return counts[r]; });
             if (!meet()) return;
             for (int g = warp; g < s.groups; g += WARPS) {
                 float e = 0.f;

@@ -258,3 +258,24 @@ def test_group_norm_refuses_overlaps():
     x, y = buf[:n].view(2, 8, 8, 16), buf[16:].view(2, 8, 8, 16)
     with pytest.raises(dcn.DcnError, match="overlaps"):
         dcn.group_norm_forward(x, None, None, 4, out=y)
+
+
+# the ring (units of several runs; a unit a sample), the queue with vectors (over 1024 channels), with single values
+@pytest.mark.parametrize("size", [(1, 300, 300, 32, 4), (160, 120, 120, 16, 2), (2, 90, 120, 1088, 64), (12, 300, 300, 3, 1),
+                                  (2, 40, 41, 64, 8)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("zeros", [1, 3, 500], ids=lambda z: "first%d" % z)
+def test_group_norm_level_behind_a_border(size, zeros):
+    """First pixels that are nothing like the others (a border of zeros before a level of 1000): the sums are not taken
+    about them for good. The mean is off by at most 64 u of the level; squares about a mean that is off by a few u of the
+    level m are off by (4 u m)^2 a value, and their sum by 64 u, so rstd by half of both."""
+    B, H, W, C, groups = size
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = 1000.0 + torch.randn((B, H * W, C), generator=g, device="cuda")
+    x[:, :zeros] = 0
+    x = x.view(B, H, W, C)
+    y, stats = dcn.group_norm_forward(x, None, None, groups, EPS, "none")
+    torch.cuda.synchronize()
+    dcn.check_status()
+    mean, rstd = ref.norm_stats(x, groups, EPS)
+    ref.check("mean", stats[..., 0], mean, 64 * ref.U * mean.abs())
+    ref.check("rstd", stats[..., 1], rstd, rstd * (64 * ref.U + (4 * ref.U * mean * rstd) ** 2))
