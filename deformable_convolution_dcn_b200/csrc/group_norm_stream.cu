@@ -144,25 +144,22 @@ struct Ring {
     volatile int* aborted;  // a wait of the block ran out: every warp leaves
 };
 
-// A barrier of some of the block's warps that none is left waiting at. After a wait that ran out warps leave one by one;
-// each arrives once more as it leaves, at the barrier that the others may be waiting at. They find `aborted` set behind
-// it, which the first to leave had set before it arrived, and leave too. (Barriers with bounded waits of their own,
-// mbarriers, took 62.5 us where this takes 59.8, 8x200x200x128.)
-struct Meet {
-    int id, threads;
-    volatile int* aborted;
-    // All lanes; false: leave.
-    __device__ __forceinline__ bool operator()() const {
-        ptx::bar_sync_named(id, threads);
-        return !__any_sync(~0u, *aborted) || leave();
-    }
-    __device__ __forceinline__ bool leave() const {
-        __threadfence_block();
-        __syncwarp();
-        ptx::bar_arrive_named(id, threads);
-        return false;
-    }
-};
+// Warps that wait by themselves for the same things (the computing warps, the joining warps) leave together when a wait of
+// one of them ran out: none stays behind at a barrier. A warp whose wait failed goes to the next agreement at once, the
+// others when they come there, all within bounded time; every way out of their loops goes through one. (Warps that leave
+// alone, with barriers that give up, cost 5 % of 8x200x200x128; with a look at a flag behind every barrier, 7 % of
+// 4096x7x7x256.)
+constexpr int COMPUTING = 1, JOINING = 2;  // named barriers
+template <int ID, int THREADS>
+__device__ __forceinline__ bool agree_to_leave(bool failed) {
+    return ptx::bar_or_named(ID, THREADS, failed);
+}
+
+template <int NC>
+__device__ __forceinline__ void sync_computing() {
+    ptx::bar_sync_named(COMPUTING, NC);
+}
+__device__ __forceinline__ void sync_joiners() { ptx::bar_sync_named(JOINING, JOINERS); }
 
 // The producer warp. MAPS: x, or x and grad_y; stats: the backward's (mean, rstd); apply: the second pass is wanted.
 template <typename T, int MAPS>
@@ -334,32 +331,27 @@ struct Post {
     }
 };
 
-// The joining warps: counts each summed unit in its set, and join(set, meet) for the sets that this block has finished
-// (false: leave).
+// The joining warps: counts each summed unit in its set, and join(set) for the sets that this block has finished.
 template <typename F>
 __device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* flag, F&& join) {
     const bool head = threadIdx.x % 32 == 0 && (int)threadIdx.x == (int)blockDim.x - JOINERS;
-    const Meet meet{2, JOINERS, ring.aborted};
     for (int n = 0;; ++n) {
         const int slot = n & 1;
         // a unit may be a long time away, the wait of the producer among the reasons
-        const bool ok = ptx::mbar_wait(ring.unit_done + slot * 8, (n >> 1) & 1, ring.aborted, a.status, 4 * WAIT_LIMIT);
-        if (!__all_sync(~0u, ok)) {
-            meet.leave();
-            return;
-        }
+        const bool ok = __all_sync(
+            ~0u, ptx::mbar_wait(ring.unit_done + slot * 8, (n >> 1) & 1, ring.aborted, a.status, 4 * WAIT_LIMIT));
         const int set = ring.unit_set[slot];
-        if (set < 0) return;
-        if (!meet()) return;
+        if (agree_to_leave<JOINING, JOINERS>(!ok || set < 0)) return;
         if (head) {
             ptx::mbar_arrive(ring.unit_free + slot * 8);
             __threadfence();
             *flag = atomicAdd(a.done + set, 1) == a.p.chunks - 1;
             __threadfence();
         }
-        if (!meet()) return;
+        sync_joiners();
         if (*flag) {
-            if (!join(set, meet) || !meet()) return;  // all of it is written
+            join(set);
+            sync_joiners();  // all of it is written
             if (head) {
                 __threadfence();
                 atomicExch(a.ready + set, 1);
@@ -370,7 +362,7 @@ __device__ __forceinline__ void join_sets(const Args& a, const Ring& ring, int* 
 
 // The forward's join: mean and rstd of a set's groups. Four threads share a group's units, each with sums about a level
 // that moves to the mean after every batch of them (see Running).
-__device__ __forceinline__ bool join_stats(const Args& a, const Meet& meet, int set, float* stats, float4* sm) {
+__device__ __forceinline__ void join_stats(const Args& a, int set, float* stats, float4* sm) {
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     const int t = threadIdx.x - (blockDim.x - JOINERS), cg = s.C / s.groups;
@@ -407,7 +399,7 @@ __device__ __forceinline__ bool join_stats(const Args& a, const Meet& meet, int 
             }
         }
         sm[t] = make_float4(n, level, m2, 0.f);
-        if (!meet()) return false;
+        sync_joiners();
         if (part == 0 && g < s.groups) {
             float4 v[JOINERS / 32];
             float e = 0.f, var = 0.f;
@@ -428,9 +420,8 @@ __device__ __forceinline__ bool join_stats(const Args& a, const Meet& meet, int 
                 stats[2 * o + 1] = out.y;
             }
         }
-        if (!meet()) return false;
+        sync_joiners();
     }
-    return true;
 }
 
 template <typename T, int ACT>
@@ -446,7 +437,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     __shared__ float4 scratch[JOINERS];
     const Ring ring = ring_of(smem, headers, bars, unit_set, &aborted, NC / 32);
     if (threadIdx.x >= NC + 32) {
-        join_sets(a, ring, &flag, [&](int set, const Meet& meet) { return join_stats(a, meet, set, stats, scratch); });
+        join_sets(a, ring, &flag, [&](int set) { join_stats(a, set, stats, scratch); });
         return;
     }
     if (threadIdx.x >= NC) {
@@ -462,8 +453,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     // each channel's group (a division each, otherwise, for every unit)
     uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
     for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
-    const Meet meet{1, NC, ring.aborted};
-    if (!meet()) return;
+    sync_computing<NC>();
     // summing: see Running; applying: k minus the mean, u rstd gamma, d beta
     Running<P> m = {};
     auto &k = m.k, &u = m.u, &d = m.d;
@@ -474,13 +464,13 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
     int stage = 0;
     uint32_t phase = 0;
     for (;;) {
-        const bool there = ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT);
-        if (!__all_sync(~0u, there)) {
-            meet.leave();
-            return;
+        const bool there =
+            __all_sync(~0u, ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT));
+        if (!there || headers[stage].pass < 0) {
+            if (agree_to_leave<COMPUTING, NC>(!there)) return;
+            break;
         }
         const Header hd = headers[stage];
-        if (hd.pass < 0) break;
         const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
         const int n = min(p.srows, s.HW - hd.row0);
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
@@ -527,11 +517,11 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
             const int slots = spread_moments<P, NC>(k, d, m.n, tx, ty, cx, ry, s.C, red, counts);
-            if (!meet()) return;
+            if (agree_to_leave<COMPUTING, NC>(false)) return;
             const float count = (float)pixels_of(a, hd.chunk);
             for (int c = threadIdx.x; c < s.C; c += NC)
                 join_slots(red + c, s.C, slots, count, [&](int r) { return counts[r]; });
-            if (!meet()) return;
+            sync_computing<NC>();
             for (int g = warp; g < s.groups; g += WARPS) {
                 float e = 0.f;
                 for (int c = lane; c < cg; c += 32) e += red[g * cg + c];
@@ -546,7 +536,7 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
                     a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.groups + g] = make_float2(mean, m2);
             }
             post(a, ring, hd.set);
-            if (!meet()) return;  // red is free
+            sync_computing<NC>();  // red is free
         }
     }
     post(a, ring, -1);
@@ -555,8 +545,8 @@ __global__ void __launch_bounds__(NC_FWD + 32 + JOINERS, 1)
 // The backward's join: the sums of a set's channels, c1 and c2 of its groups; after the last set of all, the
 // parameters' gradients. sm: [2][MAX_C].
 template <typename T>
-__device__ __forceinline__ bool join_sums(const Args& a, const Meet& meet, int set, const T* gamma, float* gg,
-                                          float* gb, float* sm, int* last) {
+__device__ __forceinline__ void join_sums(const Args& a, int set, const T* gamma, float* gg, float* gb, float* sm,
+                                          int* last) {
     const NormShape& s = a.s;
     const StreamPlan& p = a.p;
     const int t = threadIdx.x - (blockDim.x - JOINERS), warp = t / 32, lane = t % 32, cg = s.C / s.groups;
@@ -575,7 +565,7 @@ __device__ __forceinline__ bool join_sums(const Args& a, const Meet& meet, int s
         sm[c] = k * v.x;
         sm[MAX_C + c] = k * v.y;
     }
-    if (!meet()) return false;
+    sync_joiners();
     const float inv = 1.f / ((float)s.HW * (float)cg);
     for (int g = warp; g < s.groups; g += JOINERS / 32) {
         float e = 0.f, f = 0.f;
@@ -588,17 +578,16 @@ __device__ __forceinline__ bool join_sums(const Args& a, const Meet& meet, int s
         if (lane == 0) c12[(size_t)set * s.groups + g] = make_float2(e * inv, f * inv);
     }
     if (gg || gb) {
-        if (!meet()) return false;
+        sync_joiners();
         if (t == 0) {
             __threadfence();
             *last = atomicAdd(a.finished, 1) == s.B - 1;
             __threadfence();
         }
-        if (!meet()) return false;
+        sync_joiners();
         if (*last)
             for (int c = t; c < s.C; c += JOINERS) params_of(s, csums, c, gg, gb);
     }
-    return true;
 }
 
 template <typename T, int ACT>
@@ -615,9 +604,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     __shared__ float scratch[2 * MAX_C];
     const Ring ring = ring_of(smem, headers, bars, unit_set, &aborted, NC / 32);
     if (threadIdx.x >= NC + 32) {
-        join_sets(a, ring, &flag, [&](int set, const Meet& meet) {
-            return join_sums(a, meet, set, gamma, gg, gb, scratch, &last);
-        });
+        join_sets(a, ring, &flag, [&](int set) { join_sums(a, set, gamma, gg, gb, scratch, &last); });
         return;
     }
     if (threadIdx.x >= NC) {
@@ -633,8 +620,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     // each channel's group (a division each, otherwise, for every unit)
     uint16_t* group = reinterpret_cast<uint16_t*>(smem + p.stages * p.stage + RED_BYTES + MAX_C * 4);
     for (int c = threadIdx.x; c < s.C; c += NC) group[c] = (uint16_t)(c / cg);
-    const Meet meet{1, NC, ring.aborted};
-    if (!meet()) return;
+    sync_computing<NC>();
     Post post;
     Channels<P> ch = {};
     F2 u[P] = {}, d[P] = {};  // the sums, or -c1 and -c2
@@ -648,13 +634,13 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
     int stage = 0;
     uint32_t phase = 0;
     for (;;) {
-        const bool there = ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT);
-        if (!__all_sync(~0u, there)) {
-            meet.leave();
-            return;
+        const bool there =
+            __all_sync(~0u, ptx::mbar_wait(ring.full + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT));
+        if (!there || headers[stage].pass < 0) {
+            if (agree_to_leave<COMPUTING, NC>(!there)) return;
+            break;
         }
         const Header hd = headers[stage];
-        if (hd.pass < 0) break;
         const bool apply = hd.pass & 1, first_stage = hd.pass & 4, last_stage = hd.pass & 8;
         const int n = min(p.srows, s.HW - hd.row0);
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
@@ -708,7 +694,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
-            if (!meet()) return;
+            if (agree_to_leave<COMPUTING, NC>(false)) return;
             for (int c = threadIdx.x; c < s.C; c += NC) {
                 float e = 0.f, f = 0.f;
 #pragma unroll 8
@@ -719,7 +705,7 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
                 a.pieces[((size_t)hd.set * p.chunks + hd.chunk) * s.C + c] = make_float2(e, f);
             }
             post(a, ring, hd.set);
-            if (!meet()) return;  // red is free
+            sync_computing<NC>();  // red is free
         }
     }
     post(a, ring, -1);
@@ -794,6 +780,11 @@ cudaError_t norm_stream_forward(const NormShape& s, int bf, const void* x, const
     if (e != cudaSuccess) return e;
     return bf ? forward_t(a, (const bf16*)x, (const bf16*)gamma, (const bf16*)beta, (bf16*)y, stats, st)
               : forward_t(a, (const float*)x, (const float*)gamma, (const float*)beta, (float*)y, stats, st);
+}
+
+const float2* norm_stream_sums(const NormShape& s, int bf, const void* ws) {
+    const Space w = space_of(s, stream_plan(s, bf ? 2 : 4, 2), true);
+    return reinterpret_cast<const float2*>(static_cast<const uint8_t*>(ws) + w.sets);
 }
 
 cudaError_t norm_stream_backward(const NormShape& s, int bf, const void* x, const void* gamma, const void* beta,

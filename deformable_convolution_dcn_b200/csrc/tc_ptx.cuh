@@ -456,11 +456,6 @@ __device__ __forceinline__ void bar_sync_named(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
-// Arrives at a named barrier without waiting for it.
-__device__ __forceinline__ void bar_arrive_named(int id, int nthreads) {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
 // Named barrier over nthreads threads that also ORs `v` across them: every
 // participant returns the same value, so a decision taken on it is uniform.
 __device__ __forceinline__ bool bar_or_named(int id, int nthreads, bool v) {

@@ -221,15 +221,20 @@ def test_group_norm_refuses_overlaps(lib, side):
     assert bwd(q, at(1), at(2), at(3), at(4), at(5), at(6), at(7), at(7), at(9), BIG, None) == EINVAL
 
 
-def test_norm_barriers_hold_no_warp_that_others_left():
-    """In the kernel whose warps wait by themselves, hardware barriers stand in Meet alone (a warp that leaves early
-    arrives there for the others), and no way out of a failed wait goes past it."""
+def test_norm_warps_leave_together():
+    """In the kernel whose warps wait by themselves, a failed wait leads out through a barrier that all of them meet at,
+    and no bounded wait but the last (of the copies in flight) goes without the block's flag."""
     import os
     import re
     src = open(os.path.join(os.path.dirname(dcn.__file__), "csrc", "group_norm_stream.cu")).read()
-    meet = src[src.index("struct Meet {"):src.index("// The producer warp")]
-    rest = src.replace(meet, "")
-    assert "bar_sync_named" not in rest and "bar.sync" not in rest and "bar_arrive_named" not in rest
-    assert meet.count("bar_sync_named") == 1 and meet.count("bar_arrive_named") == 1
-    assert "&none" not in re.sub(r"volatile int none = 0;\n\s+for .*\n.*&none, nullptr.*", "", rest)
-    assert len(re.findall(r"if \(!__all_sync\(~0u, (?:there|ok)\)\) \{\n\s+meet\.leave\(\);\n\s+return;", rest)) == 3
+    src = re.sub(r"//[^\n]*", "", src)
+    waits = re.findall(r"mbar_wait\([^;]*;", src)
+    assert len(waits) == 7 and sum("aborted" in w for w in waits) == 6
+    # computing warps of both kernels, joining warps: decided by all, at the loop's end and at a unit's
+    assert len(re.findall(r"if \(!there \|\| headers\[stage\]\.pass < 0\) \{\s+if \(agree_to_leave<COMPUTING, NC>\(!there\)\) "
+                          r"return;\s+break;", src)) == 2
+    assert src.count("if (agree_to_leave<COMPUTING, NC>(false)) return;") == 2
+    assert src.count("if (agree_to_leave<JOINING, JOINERS>(!ok || set < 0)) return;") == 1
+    body = src[src.index("void join_sets"):src.index("template <typename F, typename... Q>")]
+    ways_out = len(re.findall(r"\breturn;", body))
+    assert ways_out == 2 + 2 + 1 + 4, ways_out  # (the kernels' dispatch of the joining and the producer warps)
