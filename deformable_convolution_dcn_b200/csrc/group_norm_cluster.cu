@@ -74,18 +74,6 @@ ClusterPlan cluster_plan(const NormShape& s, int es, int maps) {
     return p;
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
-    float v;
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [r];\n\t}"
-        : "=f"(v)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
-
 // Threads of a block over its slab: vector column cx (of tx), pixels ry, ry + ty, ...
 struct Lanes {
     int tx, ty, cx, ry;

@@ -171,6 +171,8 @@ bool norm_stream_supported(const NormShape& s, int dtype_bf16, bool backward);
 size_t norm_stream_workspace(const NormShape& s, int dtype_bf16, bool backward);
 cudaError_t norm_stream_forward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma, const void* beta,
                                 void* y, float* stats, void* ws, unsigned* status, cudaStream_t st);
+// the backward's sums [B][C] in its workspace: (sum dz, sum dz xh)
+const float2* norm_stream_sums(const NormShape& s, int dtype_bf16, const void* ws);
 cudaError_t norm_stream_backward(const NormShape& s, int dtype_bf16, const void* x, const void* gamma,
                                  const void* beta, const float* stats, const void* gy, void* gx, float* gg, float* gb,
                                  void* ws, unsigned* status, cudaStream_t st);

@@ -240,7 +240,22 @@ struct Channels {
     }
 };
 
-// grad_beta, grad_gamma: a channel's sums over the samples (sums [B][C])
+// A float in the shared memory of the cluster's CTA `rank`, at the address of its own copy.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [r];\n\t}"
+        : "=f"(v)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// grad_beta, grad_gamma: a channel's sums over the samples (sums [B][C]), by one thread: up to kFewSamples of them, by the
+// last block to join; more take params_kernel.
+constexpr int kFewSamples = 32;
 __device__ __forceinline__ void params_of(const NormShape& s, const float2* sums, int c, float* gg, float* gb) {
     float2 v = make_float2(0.f, 0.f);
 #pragma unroll 4

@@ -279,3 +279,17 @@ def test_group_norm_level_behind_a_border(size, zeros):
     mean, rstd = ref.norm_stats(x, groups, EPS)
     ref.check("mean", stats[..., 0], mean, 64 * ref.U * mean.abs())
     ref.check("rstd", stats[..., 1], rstd, rstd * (64 * ref.U + (4 * ref.U * mean * rstd) ** 2))
+
+
+# by clusters, by the ring, by the queue (channels that are not whole vectors), and a few samples of each
+@pytest.mark.parametrize("size", [(20000, 2, 2, 64, 8), (4096, 7, 7, 72, 8), (70000, 1, 1, 40, 8), (300, 45, 45, 512, 32),
+                                  (3000, 3, 3, 33, 3), (33, 2, 2, 40, 8), (65, 2, 2, 40, 8), (64, 3, 3, 33, 3),
+                                  (40, 100, 100, 64, 8)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_group_norm_parameters_of_many_samples(size, dtype):
+    """Equal samples with a constant grad_y, whose sums round the same way each time: no chain grows with them."""
+    B, H, W, C, groups = size
+    d = make(1, H, W, C, dtype, seed=14)
+    d["x"] = d["x"].expand(B, H, W, C).contiguous()
+    d["gy"] = torch.full_like(d["x"], 1.013)
+    check_backward(d, groups, "none")
