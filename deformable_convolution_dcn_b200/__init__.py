@@ -677,6 +677,8 @@ class LinearFunction(torch.autograd.Function):
 
 def linear(x, weight, bias=None, residual=None, activation="none"):
     """Differentiable act(x W^T + bias + residual); shapes as for linear_forward."""
+    if not torch.is_grad_enabled():  # nothing is kept for a backward pass, whatever the parameters require
+        return linear_forward(x, weight, bias, residual, activation)
     return LinearFunction.apply(x, weight, bias, residual, activation)
 
 

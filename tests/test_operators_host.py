@@ -238,3 +238,22 @@ def test_norm_warps_leave_together():
     body = src[src.index("void join_sets"):src.index("template <typename F, typename... Q>")]
     ways_out = len(re.findall(r"\breturn;", body))
     assert ways_out == 2 + 2 + 1 + 4, ways_out  # (the kernels' dispatch of the joining and the producer warps)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode, torch.enable_grad])
+@pytest.mark.parametrize("activation", ["silu", "gelu"])
+def test_linear_keeps_the_preactivation_only_for_a_backward_pass(monkeypatch, mode, activation):
+    asked = []
+
+    def forward(x, weight, bias=None, residual=None, activation="none", *, need_preact=False, **kw):
+        asked.append(need_preact)
+        y = x @ weight.t()
+        return (y, y.clone()) if need_preact else y
+
+    monkeypatch.setattr(dcn, "linear_forward", forward)
+    x, w = torch.ones(3, 4), torch.ones(5, 4, requires_grad=True)
+    with mode():
+        y = dcn.linear(x, w, None, None, activation)
+    assert asked == [mode is torch.enable_grad] and y.requires_grad == (mode is torch.enable_grad)
+    dcn.linear(x, w.detach(), None, None, activation)  # gradients recorded, none required
+    assert asked[-1] is False
