@@ -12,7 +12,8 @@
 // in three bfloat16 terms a0 + a1 + a2 (24 bits), and the product is
 // a0 b0 + (a0 b1 + a1 b0 + a1 b1 + a0 b2 + a2 b0); the terms left out are below
 // 2^-26 of a b. a0 b0 has an accumulator of its own, so that the small products
-// do not make it round more often. The tensor cores cut each step's sum off
+// do not make it round more often, and stands alone where it is infinite or NaN:
+// an infinity has zeros for its other terms, whose products would make it NaN. The tensor cores cut each step's sum off
 // rather than rounding it, so float32 results take the accumulator out every
 // `chunk` blocks of 64 and add it in registers with proper rounding.
 //
@@ -621,7 +622,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                             float l[32];
                             ptx::tmem_ld32(from + 128 + j, l);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += l[i];
+                            for (int i = 0; i < 32; ++i) {
+                                const float sum = v[i] + l[i];
+                                v[i] = fabsf(v[i]) <= 3.4028234663852886e38f ? sum : v[i];
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[j + i] += v[i];

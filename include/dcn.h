@@ -257,9 +257,8 @@ typedef enum {
  *   x [M, K], weight [N, K], bias [N] or NULL, residual [M, N] or NULL, y [M, N]
  * all in `dtype`. Sums, bias, residual and activation are float32; z and y are
  * rounded once each. float32 layers keep float32 accuracy on the tensor cores
- * (operands split in three bfloat16 terms). Infinities and NaN of a bfloat16
- * layer spread as in the sums above; a float32 layer may turn an infinity into
- * NaN. M may be 0; M, N, K up to 2^30, each tensor below 2^31 elements. */
+ * (operands split in three bfloat16 terms). Infinities and NaN spread as in the
+ * sums above. M may be 0; M, N, K up to 2^30, each tensor below 2^31 elements. */
 typedef struct {
     int M, N, K;
     int act;         /* dcn_act_t */

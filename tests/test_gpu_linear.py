@@ -295,3 +295,42 @@ def test_linear_one_output(size, dtype, residual):
     if residual:
         dcn.linear_forward(x, w, room[:1], r, "relu", out=r)
         assert torch.equal(r, y)
+
+
+def spread_of(t):
+    """0 where finite, 1 and -1 for the infinities, 2 for NaN."""
+    return torch.where(torch.isnan(t), 2.0, torch.where(torch.isinf(t), torch.sign(t), 0.0)).cpu()
+
+
+@pytest.mark.parametrize("size", [(8, 72, 64), (9, 72, 64), (150, 72, 64), (150, 72, 67), (2500, 8, 24), (33, 24, 4104),
+                                  (40000, 64, 64)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_linear_infinities_spread_as_in_the_sums(size, dtype):
+    """The same signs and NaN as the products' sums, whatever the number of rows."""
+    M, N, K = size
+    d = make(M, N, K, dtype, seed=15)
+    inf = float("inf")
+    d["x"][1, 3], d["x"][2, 0], d["x"][2, 1], d["x"][3, 0], d["x"][3, 2], d["x"][5, 4] = inf, inf, inf, inf, -inf, -inf
+    d["w"][4, 3], d["w"][6, 5], d["gy"][7, 2], d["gy"][0, 4] = 0.0, -inf, inf, -inf  # (0 times infinity is NaN)
+    d["w"][2, 6] = 1.0  # exact in one term
+    y = dcn.linear_forward(d["x"], d["w"], d["b"], d["r"], "none")
+    gx, gw, gb, gr = dcn.linear_backward(d["x"], d["w"], None, d["gy"], "none", need_residual=True)
+    torch.cuda.synchronize()
+    dcn.check_status()
+    # the sums in float64 on the CPU (a product at a time: a library product need not keep the signs)
+    x, w, gy = (d[k].double().cpu() for k in ("x", "w", "gy"))
+    rows = slice(0, 12)
+    want = (x[rows, None, :] * w).sum(-1) + (d["b"].double() + d["r"].double()[rows]).cpu()
+    assert torch.equal(spread_of(y[rows]), spread_of(want).to(y.dtype))
+    assert torch.isfinite(y[12:, :6]).all() and torch.isfinite(y[12:, 7:]).all()
+    want = (gy[rows, :, None] * w).sum(1)
+    assert torch.equal(spread_of(gx[rows]), spread_of(want).to(gx.dtype))
+    want = torch.stack([(gy[:, n, None] * x).sum(0) for n in range(8)])
+    assert torch.equal(spread_of(gw[:8]), spread_of(want).float())
+    assert torch.equal(spread_of(gb), spread_of(gy.sum(0)).float()) and torch.equal(gr, d["gy"])
+    # silu and gelu: grad_weight of a bfloat16 layer splits dz
+    z = make(M, N, K, dtype, seed=16)["r"]
+    gw = dcn.linear_backward(d["x"], d["w"], z, d["gy"], "gelu")[1]
+    dz = gy * ref.slope(z.double().cpu(), "gelu")
+    want = torch.stack([(dz[:, n, None] * x).sum(0) for n in range(8)])
+    assert torch.equal(spread_of(gw[:8]), spread_of(want).float())
