@@ -15,7 +15,10 @@
 // do not make it round more often, and stands alone where it is infinite or NaN:
 // an infinity has zeros for its other terms, whose products would make it NaN. The tensor cores cut each step's sum off
 // rather than rounding it, so float32 results take the accumulator out every
-// `chunk` blocks of 64 and add it in registers with proper rounding.
+// `chunk` blocks of 64 and add it in registers with proper rounding. bfloat16
+// results leave the whole reduction in the accumulator: cut off they lose 5.8e-5
+// of 12544 positive products, 1.6e-4 of 65536 and 8.6e-4 of 401408 (of products of
+// both signs a quarter of that), their rounding is off by up to 2e-3.
 //
 // Warps: 0 and 10 TMA producers of A and B, 1 MMA issue and TMEM, 2-9 epilogue
 // (each of the four TMEM lane quarters twice, once for each half of the columns). Accumulators
@@ -1216,7 +1219,10 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
     p.pack_x = p.pack_w = !xw;
     p.pass_dz = !gy;
     p.dz_terms = dz_terms(bf, smooth);
-    // grad_x of a bfloat16 layer reads the first term alone: dz rounded once, as a grad_x in bfloat16 is
+    // grad_x of a bfloat16 layer reads the first term alone: dz rounded to bfloat16 once, as it is where a framework
+    // stores it between the activation's gradient and the product. It is then 1.4 times as far from the exact one as its
+    // own rounding (2.3e-3 and 1.66e-3 by norm). Two terms would leave the rounding alone, at 95.5 us instead of 78.6 for
+    // the backward of 5000x2048x512 gelu, 69.2 instead of 59.1 for 5000x512x2048 silu.
     p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4, kActNone);
     p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4, kActNone);
     const int c8 = up8(s.N) / 8;
