@@ -86,7 +86,7 @@ struct GemmArgs {
     const void *bias, *residual;
     void *y, *z;
     int act;
-    int swapped;           // D's rows are the result's columns (a row stride of 1 does not say so: one column has it too)
+    int one_column;        // the result has one, and one bias: swapped, D is walked as if it were not (cs = 1)
     int tma_out;           // D's rows are 16-byte aligned and written as they lie: TMA stores
     int nslots;            // chunks a warp stages (tma_out)
     uint32_t slot_off, sm_off;  // the epilogue's slots or exchange buffers; its bias
@@ -269,13 +269,11 @@ struct Emit {
 #pragma unroll
         for (int i = 0; i < 32; ++i) sm[lane * 33 + i] = v[i];
         __syncwarp();
-        const bool rows_on_lanes = a.cs != 1;  // (swapped: a result of one column is walked along D's columns all the same)
+        const bool rows_on_lanes = a.cs != 1;
         const int mine = (rows_on_lanes ? row0 : col) + lane;  // this lane's row or column
         const int n = min(32, rows_on_lanes ? a.cols - col : a.rows - row0);
         if (mine < (rows_on_lanes ? a.rows : a.cols)) {
-            // the bias is the lane's, or the loop's where D is swapped and walked along its columns
-            const T* each = bias && a.swapped && !rows_on_lanes ? bias + row0 : nullptr;
-            const float b = bias && !each ? ld1(bias + mine) : 0.f;
+            const float b = bias ? ld1(bias + (a.one_column ? 0 : mine)) : 0.f;
             long long at = rows_on_lanes ? mine + col * a.cs : row0 * a.rs + mine;
             const long long step = rows_on_lanes ? a.cs : a.rs;
             const float* p = rows_on_lanes ? sm + lane * 33 : sm + lane;
@@ -283,7 +281,7 @@ struct Emit {
             T* yp = y + sp * a.part;
 #pragma unroll 4
             for (int i = 0; i < n; ++i, at += step) {
-                float s = p[i * ps] + (each ? ld1(each + i) : b);
+                float s = p[i * ps] + b;
                 if (residual) s += ld1(residual + at);
                 if (z) z[at] = from_float<T>(s);
                 yp[at] = from_float<T>(act_run<kFast<T>>(s, a.act));
@@ -1091,7 +1089,7 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
     a.stage_bytes = L.terms * A_BYTES + R.terms * (uint32_t)(p.bn / p.cg) * 128;
     a.status = status;
     a.gb = sums;
-    a.swapped = p.swap;
+    a.one_column = cols == 1;
     const bool split = p.splits > 1;
     const int pitch = split ? (cols + 7) / 8 * 8 : cols;
     a.rs = p.swap ? 1 : pitch;
