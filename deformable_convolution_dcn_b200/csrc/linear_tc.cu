@@ -61,7 +61,7 @@ constexpr long long WAIT_LIMIT = 2000000000LL;
 // How the TMA producer walks an operand (see encode()).
 constexpr int kKMajor = 0, kMnBlocks = 1, kMnRows = 2;
 struct Operand {
-    int terms;  // bfloat16 terms: 1 or 3
+    int terms;  // bfloat16 terms: 1 or 3 (A of a bfloat16 result: or 2)
     int kind;
 };
 
@@ -417,10 +417,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int x = x0 + kb * dx, y = y0 + kb * dy;
                     if (o.kind != kMnRows) {
                         ptx::tma_load_4d_cg<CG>(dst, map, bar, x, y, z0, 0);
-                        if (o.terms > 1) {
-                            ptx::tma_load_4d_cg<CG>(dst + term_bytes, map, bar, x, y, z0, 1);
-                            ptx::tma_load_4d_cg<CG>(dst + 2 * term_bytes, map, bar, x, y, z0, 2);
-                        }
+                        if (o.terms > 1) ptx::tma_load_4d_cg<CG>(dst + term_bytes, map, bar, x, y, z0, 1);
+                        if (o.terms > 2) ptx::tma_load_4d_cg<CG>(dst + 2 * term_bytes, map, bar, x, y, z0, 2);
                     } else {
                         for (int t = 0; t < o.terms; ++t)
                             for (int h = 0; h < rows / 64; ++h)
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const OperandDesc da(base, a_mn), db(base + a.a.terms * A_BYTES, b_mn);
             const uint32_t aterm = A_BYTES / 16, bterm = (uint32_t)(a.bn / CG) * 128 / 16;
             const uint32_t stage_units = a.stage_bytes / 16;
-            const bool many = a.a.terms > 1, both = a.b.terms > 1;
+            const bool one = a.a.terms == 1, two = PB == 0 && a.a.terms == 2, both = a.b.terms > 1;
             int stage = 0;
             uint32_t phase = 0, acc_phase = 1, off = 0;
             int buf = 0;
@@ -470,10 +468,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ptx::tc_fence_after();
                         if (ptx::elect_one()) {
                             const uint32_t first = kb > c0;
-                            if (!many) {
+                            if (one) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     ptx::mma_bf16_cg<CG>(acc, da.at(off, k), db.at(off, k), idesc, k ? 1u : first);
+                            } else if (two) {  // a bfloat16 result: one accumulator for both
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint64_t b0 = db.at(off, k);
+                                    ptx::mma_bf16_cg<CG>(acc, da.at(off, k), b0, idesc, k ? 1u : first);
+                                    ptx::mma_bf16_cg<CG>(acc, da.at(off + aterm, k), b0, idesc, 1u);
+                                }
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -1008,7 +1013,7 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
         const int sa = swap ? tb : ta, sb = swap ? ta : tb;
         if (sa < sb) continue;  // the kernel takes the split operand as A
         for (int cg = 1; cg <= 2; ++cg)
-            for (int bn = 64; bn <= (prods > 1 ? 128 : 256); bn *= 2) {
+            for (int bn = 64; bn <= (prods > 2 ? 128 : 256); bn *= 2) {
                 if (cg == 2 && bn < 128) continue;
                 if (bn > 64 && bn / 2 >= c) continue;
                 if (prods == 6 && cg == 1 && bn == 128) continue;  // shared memory holds one stage only
@@ -1028,7 +1033,8 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
                     double t = waves * (std::max(kb * stage, splits > 1 ? part : epi) + 700.0) +
                                (splits > 1 ? part : epi) + 2000.0;
                     if (splits > 1) t += 4000.0 + (double)rows * cols * (4.0 * splits + out_bytes) / (sms * 12.0);
-                    if (t < best_t) {
+                    // (on a tie pairs, for the L2's sake: grad_x of 5000x2048x512 silu 45 us, with single CTAs 53)
+                    if (t < best_t || (t == best_t && cg > best.cg)) {
                         best_t = t;
                         best = {swap != 0, cg, bn, splits, 0};
                     }
@@ -1208,6 +1214,11 @@ struct BwdPlan {
 // grad_weight was 10 times as far from the exact one.)
 constexpr int dz_terms(int bf, bool smooth) { return bf && !smooth ? 1 : 3; }
 
+// And how many grad_x takes: the two first of three for a bfloat16 result, whose rounding hides the third (2^-18 of dz).
+// (With dz rounded to one, the backward of 5000x2048x512 gelu takes 78.6 us instead of 87.9, but grad_x is 1.4 to 1.5 times
+// as far from the exact one.)
+constexpr int gx_terms(int bf, bool smooth) { return bf ? (smooth ? 2 : 1) : 3; }
+
 BwdPlan plan_backward(const LinearShape& s, int bf) {
     BwdPlan p = {};
     const int terms = bf ? 1 : 3;
@@ -1217,11 +1228,7 @@ BwdPlan plan_backward(const LinearShape& s, int bf) {
     p.pack_x = p.pack_w = !xw;
     p.pass_dz = !gy;
     p.dz_terms = dz_terms(bf, smooth);
-    // grad_x of a bfloat16 layer reads the first term alone: dz rounded to bfloat16 once, as it is where a framework
-    // stores it between the activation's gradient and the product. It is then 1.4 times as far from the exact one as its
-    // own rounding (2.3e-3 and 1.66e-3 by norm). Two terms would leave the rounding alone, at 95.5 us instead of 78.6 for
-    // the backward of 5000x2048x512 gelu, 69.2 instead of 59.1 for 5000x512x2048 silu.
-    p.gx = plan_gemm(s.M, s.K, s.N, terms, terms, !bf, bf ? 2 : 4, kActNone);
+    p.gx = plan_gemm(s.M, s.K, s.N, gx_terms(bf, smooth), terms, !bf, bf ? 2 : 4, kActNone);
     p.gw = plan_gemm(s.N, s.K, s.M, p.dz_terms, terms, true, 4, kActNone);
     const int c8 = up8(s.N) / 8;
     p.tx = std::min(c8, 256);
@@ -1317,7 +1324,7 @@ cudaError_t backward_t(const LinearShape& s, const T* x, const T* w, const T* sa
     const Sums sums{(const float*)(ws + p.sums), p.rblocks, up8(s.N), s.N, gb};
     if (gx) {
         Matrix first = DZ;
-        first.terms = terms;
+        first.terms = gx_terms(bf, s.act == kActSilu || s.act == kActGelu);
         e = run_gemm<T>(p.gx, first, false, W, true, s.M, s.K, s.N, Out<T>{nullptr, nullptr, gx, nullptr, kActNone},
                         (float*)(ws + p.parts), !bf, gw ? Sums{} : sums, status, st, launches);
         if (e != cudaSuccess) return e;

@@ -334,3 +334,25 @@ def test_linear_infinities_spread_as_in_the_sums(size, dtype):
     dz = gy * ref.slope(z.double().cpu(), "gelu")
     want = torch.stack([(dz[:, n, None] * x).sum(0) for n in range(8)])
     assert torch.equal(spread_of(gw[:8]), spread_of(want).float())
+
+
+@pytest.mark.parametrize("size", [(300, 264, 72), (1000, 2056, 136), (9, 40, 24), (5000, 512, 256), (129, 65, 513),
+                                  (20000, 264, 520)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_linear_grad_x_of_bfloat16_does_not_round_dz(size, act):
+    """grad_x = dz W is rounded once, at its end: two bfloat16 terms of dz leave out at most 2^-18 of it."""
+    M, N, K = size
+    d = make(M, N, K, "bf16", seed=17)
+    saved = d["r"]
+    gx = dcn.linear_backward(d["x"], d["w"], saved, d["gy"], act, need_weight=False, need_bias=False)[0]
+    torch.cuda.synchronize()
+    dcn.check_status()
+    w, gy, z = d["w"].double(), d["gy"].double(), saved.double()
+    dz = gy * ref.slope(z, act)
+    want = dz @ w
+    edz = 16 * ref.U * gy.abs() * (1 + z.abs()) + 2.0 ** -18 * dz.abs()
+    err = (N + 16) * ref.U * (dz.abs() @ w.abs()) + edz @ w.abs()
+    ref.check("grad_x", gx, want, err + ref.half_step(torch.bfloat16) * (want.abs() + err))
+    # as far from the exact one as its rounding alone
+    rounded = (want.bfloat16().double() - want).norm()
+    assert float((gx.double() - want).norm()) <= 1.05 * float(rounded)
