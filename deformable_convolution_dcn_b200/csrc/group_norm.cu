@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(NT, 2)
             mean[i] = __ldg(st);
             rstd[i] = __ldg(st + 1);
         }
-        // f(r, dz values, xh values) for each of the thread's pixels
-        auto walk = [&](auto&& f) {
+        // f(r, dz values, xh values) for each of the thread's pixels, after(n) behind n of them
+        auto walk = [&](auto&& f, auto&& after) {
             auto one = [&](int row, const float(&v)[V], const float(&g)[V]) {
                 float d[V], hat[V];
 #pragma unroll
@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(NT, 2)
                         unpack(g, h[j]);
                         one(r + j * ty, v, g);
                     }
+                    after(4);
                     r += 4 * ty;
                     ahead = fetch();
                 }
@@ -627,22 +628,39 @@ __global__ void __launch_bounds__(NT, 2)
                 load<T, V>(v, x + at + (size_t)r * s.C);
                 load<T, V>(g, gy + at + (size_t)r * s.C);
                 one(r, v, g);
+                after(1);
             }
         };
         if (pass == 0) {
             if (in) {
-                float s1[V] = {}, s2[V] = {};
-                walk([&](int, const float(&d)[V], const float(&hat)[V]) {
+                // sums of kRun pixels, and sums of those: no chain grows with the map
+                float s1[V] = {}, s2[V] = {}, t1[V] = {}, t2[V] = {};
+                int run = 0;
+                auto close = [&]() {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        s1[i] += d[i];
-                        s2[i] = fmaf(d[i], hat[i], s2[i]);
+                        t1[i] += s1[i];
+                        t2[i] += s2[i];
+                        s1[i] = s2[i] = 0.f;
                     }
-                });
+                    run = 0;
+                };
+                walk(
+                    [&](int, const float(&d)[V], const float(&hat)[V]) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            s1[i] += d[i];
+                            s2[i] = fmaf(d[i], hat[i], s2[i]);
+                        }
+                    },
+                    [&](int n) {
+                        if ((run += n) >= kRun) close();
+                    });
+                close();
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sm[ry * p.cb + cx * V + i] = s1[i];
-                    sm[(ty + ry) * p.cb + cx * V + i] = s2[i];
+                    sm[ry * p.cb + cx * V + i] = t1[i];
+                    sm[(ty + ry) * p.cb + cx * V + i] = t2[i];
                 }
             }
             __syncthreads();
@@ -674,7 +692,7 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] = rstd[i] * (fmaf(ga[i], d[i], -c1[i]) - hat[i] * c2[i]);
                 store<T, V>(gx + at + (size_t)row * s.C, v);
-            });
+            }, [](int) {});
         }
     }
 }

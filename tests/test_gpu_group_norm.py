@@ -293,3 +293,22 @@ def test_group_norm_parameters_of_many_samples(size, dtype):
     d["x"] = d["x"].expand(B, H, W, C).contiguous()
     d["gy"] = torch.full_like(d["x"], 1.013)
     check_backward(d, groups, "none")
+
+
+# the ring, the queue with vectors and with single values: thousands of pixels a thread
+@pytest.mark.parametrize("size", [(16, 200, 200, 512, 32), (150, 160, 160, 64, 8), (2, 500, 500, 1088, 64), (1, 700, 700, 1025, 1),
+                                  (1, 1000, 1000, 512, 32)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("value", [1.013, 1.1])
+def test_group_norm_constant_gradients_of_large_maps(size, value):
+    """The mean's gradient, the same everywhere, rounds the same way at each step of a sum: no chain grows with the map.
+    (Runs of 64, chains of up to 130 runs, at most 512 units: 64 u, as for any gradient.)"""
+    B, H, W, C, groups = size
+    x = torch.randn((B, H, W, C), generator=torch.Generator(device="cuda").manual_seed(24), device="cuda")
+    gy = torch.full_like(x, value)
+    ga, be = torch.ones(C, device="cuda"), torch.zeros(C, device="cuda")
+    stats = torch.stack(ref.norm_stats(x, groups, EPS), dim=-1).float()
+    gx, gg, gb = dcn.group_norm_backward(x, ga, be, stats, gy, groups)
+    torch.cuda.synchronize()
+    dcn.check_status()
+    want = float(gy.flatten()[0]) * B * H * W
+    ref.check("grad_beta", gb, torch.full_like(gb, want, dtype=torch.float64), torch.full_like(gb, 64 * ref.U * want))

@@ -233,11 +233,11 @@ def test_norm_warps_leave_together():
     # computing warps of both kernels, joining warps: decided by all, at the loop's end and at a unit's
     assert len(re.findall(r"if \(!there \|\| headers\[stage\]\.pass < 0\) \{\s+if \(agree_to_leave<COMPUTING, NC>\(!there\)\) "
                           r"return;\s+break;", src)) == 2
-    assert src.count("if (agree_to_leave<COMPUTING, NC>(false)) return;") == 2
+    assert src.count("if (agree_to_leave<COMPUTING, NC>(false)) return;") == 3
     assert src.count("if (agree_to_leave<JOINING, JOINERS>(!ok || set < 0)) return;") == 1
     body = src[src.index("void join_sets"):src.index("template <typename F, typename... Q>")]
     ways_out = len(re.findall(r"\breturn;", body))
-    assert ways_out == 2 + 2 + 1 + 4, ways_out  # (the kernels' dispatch of the joining and the producer warps)
+    assert ways_out == 2 + 3 + 1 + 4, ways_out  # (the kernels' dispatch of the joining and the producer warps)
 
 
 @pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode, torch.enable_grad])
