@@ -855,7 +855,8 @@ cudaError_t backward_t(const NormShape& s, bool vec, const T* x, const T* gamma,
 namespace {
 
 // Which kernels an aligned map goes to. Clusters need one launch; the queue with a ring, two, moves large maps faster:
-// relu on 8x50x50x256 11.5 and 18.5 us, on 8x80x80x256 (26 MB) 27.7 and 25.0 us, on 64x28x28x512 48 and 35 us.
+// relu on 8x50x50x256 11.5 and 18.5 us, on 8x80x80x256 (26 MB) 28.2 and 27.5 us, on 64x28x28x512 51 and 37 us, on
+// 4096x7x7x256 197 and 161.
 // (Backward the clusters lead wherever they fit: 64x28x28x512 82 and 118 us.)
 enum class Path { cluster, stream, queue };
 Path path_of(const NormShape& s, int bf, bool backward) {

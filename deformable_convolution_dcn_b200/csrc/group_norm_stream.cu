@@ -7,11 +7,12 @@
 // of one stage, to a ring of shared-memory stages (bulk copies, up to 160 KB in
 // flight); most warps compute from there and store; four more warps count the summed
 // units and join their sets. So the memory works on while sums are counted, joined and
-// released, and those latencies cost little (bfloat16: 8x200x200x128 silu 59 us,
-// 8x100x100x256 relu backward 69, both bound by the instructions of the computing warps,
-// 36 to 46 % of the issue slots with one block an SM, and by the waits between the passes): with the fence and the atomic in a
+// released, and those latencies cost little: with the fence and the atomic in a
 // computing warp a unit cost nine microseconds more, in a kernel without the ring
-// (group_norm.cu) 8x200x200x128 takes 92 us. The producer waits for a set's statistics
+// (group_norm.cu) 8x200x200x128 takes 92 us. bfloat16 8x200x200x128 silu takes 59 us,
+// 8x100x100x256 relu backward 68.5, with 36 to 46 % of the issue slots and about as much
+// of HBM's rate used: the rest is waiting, of the second pass for all sums, and of one
+// block an SM for its own joins. The producer waits for a set's statistics
 // before it copies a unit of the second pass, and leaves them in its first stage.
 //
 // A claimed unit waits for none but lower ones, which are summed by blocks that
@@ -61,8 +62,9 @@ StreamPlan stream_plan(const NormShape& s, int es, int maps) {
     p.stage = (maps * (p.data + s.groups * 8) + 127) / 128 * 128;
     p.stages = (int)std::min<uint32_t>(MAX_STAGES, RING / p.stage);
     // A unit costs a few microseconds beside its pixels (reduction, join, wait), so the sets are cut in as many units as
-    // there are SMs and no more: 8x100x100x256 backward takes 58 us, with twice the units, which L2 would hold until
-    // their second pass, 74 us; forward the two are even (8x200x200x128 without activation: 51.5 and 49.5 us).
+    // there are SMs. Twice as many, of which L2 holds more until their second pass, are better or worse by the activation:
+    // backward 8x100x100x256 51.7 us (twice the units: 56.8) without one, 68.5 (63) with relu; forward 8x200x200x128 51.7
+    // (49.6) without, 59.6 (54.2) with silu.
     const int chunks = s.B <= 74 ? 148 / s.B : s.B < 148 ? 2 : 1;
     p.blocks = (s.HW + p.srows - 1) / p.srows;
     p.chunks = std::min(chunks, p.blocks);

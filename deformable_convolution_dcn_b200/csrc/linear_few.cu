@@ -2,16 +2,18 @@
 // one pixel), in one launch on CUDA cores: y = act(x W^T + bias + residual).
 //
 // Such a product reads the weight once and does next to nothing with it, so it is
-// bound by the weight's bytes and by latency. A block walks groups of NR rows of W
-// (x then comes from L1 after the first group); its warps share the reduction
-// (each lane a 16-byte vector of every row at a time), so that the loads of a block lie side by side and no part of a sum leaves it.
-// Sums are float32 pairs (fma.f32x2), joined by a butterfly over the lanes and
-// then over the warps, in a fixed order.
+// bound by the weight's bytes and by latency. A block's warps form teams of one to
+// eight; a team takes a group of NR rows of W at a time and shares its reduction
+// (each lane a 16-byte vector of every row at a time), so that its loads lie side by
+// side, no part of a sum leaves the block, and x comes from L1 after the first group,
+// for all teams. Sums are float32 pairs (fma.f32x2), joined by a butterfly over the
+// lanes and then over the team's warps, in a fixed order.
 //
-// N x K of 1024 x 12544 bfloat16 (25.7 MB, 3.9 us at HBM rate): 5.8 to 6.7 us for one
-// row, 8.2 for two, 10.9 for five, 12.8 for eight, where x's loads and the sums bound
-// it. The tensor-core kernel, with its reduction split 18 times and a joining launch,
-// takes 13.3 us. float32: 10.3 us for one row, 22.8 for eight, tensor cores 45.2.
+// N x K of 1024 x 12544 bfloat16 (25.7 MB, 3.9 us at HBM rate): 6 to 7 us for one
+// row, 8.5 for two, 11 to 12 for five, 13.6 for eight: the more rows, the more of the
+// time goes to x's loads (two of the weight's rows for each of them) and the sums. The
+// tensor-core kernel, with its reduction split 18 times and a joining launch, takes
+// 13.5 us for nine. float32: 10.4 us for one row, 23 for eight, tensor cores 45.2.
 #include <algorithm>
 #include <type_traits>
 

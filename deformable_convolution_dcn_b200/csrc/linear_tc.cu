@@ -27,11 +27,12 @@
 // 32-byte sectors. Products with too few tiles to fill the GPU are split along
 // the reduction; the parts meet in finish_kernel, in a fixed order.
 //
-// Measured (M x N x K, GPU time): bfloat16 4000x1024x12544 relu 72 us, 1426 TFLOP/s,
-// the tensor pipe busy 86 % of the cycles; 20000x1024x256 14.4 us, bound by the
-// result's bytes, and 24.8 with relu and a shortcut; backward 20000x256x1024 51 us,
-// 5000x2048x512 gelu 77 us, of which the preparation of dz takes 13 to 18; float32
-// 8192x2048x2048 297 us, 1387 TFLOP/s of bfloat16 products (power-bound).
+// Measured (M x N x K, GPU time): bfloat16 4000x1024x12544 relu 73 us, 1410 TFLOP/s,
+// the tensor pipe busy 86 % of the cycles, backward 180; 20000x1024x256 18 us, bound by
+// the result's bytes (14.4 where L2 holds x), and 25.5 with relu and a shortcut; backward
+// 20000x256x1024 relu 53 us, 5000x2048x512 gelu 87 us, of which the preparation of dz takes
+// 13 to 18; float32 8192x2048x2048 293 to 310 us, 1350 TFLOP/s of bfloat16 products
+// (power-bound).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
