@@ -153,9 +153,8 @@ struct Ring {
 // Warps that wait by themselves for the same things (the computing warps, the joining warps) leave together when a wait of
 // one of them ran out: none stays behind at a barrier. A warp whose wait failed goes to the next agreement at once, the
 // others when they come there, all within bounded time: the first barrier behind a wait is always one, and so is every way
-// out of their loops. (Warps that leave
-// alone, with barriers that give up, cost 5 % of 8x200x200x128; with a look at a flag behind every barrier, 7 % of
-// 4096x7x7x256.)
+// out of their loops. (Warps that leave alone, with barriers that give up, cost 5 % of 8x200x200x128; with a look at a flag
+// behind every barrier, 7 % of 4096x7x7x256.)
 constexpr int COMPUTING = 1, JOINING = 2;  // named barriers
 template <int ID, int THREADS>
 __device__ __forceinline__ bool agree_to_leave(bool failed) {

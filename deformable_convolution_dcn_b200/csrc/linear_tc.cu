@@ -62,7 +62,7 @@ constexpr long long WAIT_LIMIT = 2000000000LL;
 // How the TMA producer walks an operand (see encode()).
 constexpr int kKMajor = 0, kMnBlocks = 1, kMnRows = 2;
 struct Operand {
-    int terms;  // bfloat16 terms: 1 or 3 (A of a bfloat16 result: or 2)
+    int terms;  // bfloat16 terms: 1 or 3 (one side of a bfloat16 result: or 2)
     int kind;
 };
 
@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const OperandDesc da(base, a_mn), db(base + a.a.terms * A_BYTES, b_mn);
             const uint32_t aterm = A_BYTES / 16, bterm = (uint32_t)(a.bn / CG) * 128 / 16;
             const uint32_t stage_units = a.stage_bytes / 16;
-            const bool one = a.a.terms == 1, two = PB == 0 && a.a.terms == 2, both = a.b.terms > 1;
+            const bool one = a.a.terms * a.b.terms == 1, two = PB == 0 && a.a.terms * a.b.terms == 2, both = a.b.terms > 1;
+            const uint32_t a2 = a.a.terms == 2 ? aterm : 0, b2 = aterm == a2 ? 0 : bterm;  // of two: the second product's
             int stage = 0;
             uint32_t phase = 0, acc_phase = 1, off = 0;
             int buf = 0;
@@ -476,9 +477,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             } else if (two) {  // a bfloat16 result: one accumulator for both
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
-                                    const uint64_t b0 = db.at(off, k);
-                                    ptx::mma_bf16_cg<CG>(acc, da.at(off, k), b0, idesc, k ? 1u : first);
-                                    ptx::mma_bf16_cg<CG>(acc, da.at(off + aterm, k), b0, idesc, 1u);
+                                    ptx::mma_bf16_cg<CG>(acc, da.at(off, k), db.at(off, k), idesc, k ? 1u : first);
+                                    ptx::mma_bf16_cg<CG>(acc, da.at(off + a2, k), db.at(off + b2, k), idesc, 1u);
                                 }
                             } else {
 #pragma unroll
@@ -1012,7 +1012,7 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
     for (int swap = 0; swap < 2; ++swap) {
         const long long r = swap ? cols : rows, c = swap ? rows : cols;
         const int sa = swap ? tb : ta, sb = swap ? ta : tb;
-        if (sa < sb) continue;  // the kernel takes the split operand as A
+        if (sa < sb && sb > 2) continue;  // the kernel takes the operand in three terms as A
         for (int cg = 1; cg <= 2; ++cg)
             for (int bn = 64; bn <= (prods > 2 ? 128 : 256); bn *= 2) {
                 if (cg == 2 && bn < 128) continue;

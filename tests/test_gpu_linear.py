@@ -337,7 +337,7 @@ def test_linear_infinities_spread_as_in_the_sums(size, dtype):
 
 
 @pytest.mark.parametrize("size", [(300, 264, 72), (1000, 2056, 136), (9, 40, 24), (5000, 512, 256), (129, 65, 513),
-                                  (20000, 264, 520)], ids=lambda s: "x".join(map(str, s)))
+                                  (20000, 264, 520), (5, 1024, 12544), (64, 512, 4096), (2, 300, 2056)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_linear_grad_x_of_bfloat16_does_not_round_dz(size, act):
     """grad_x = dz W is rounded once, at its end: two bfloat16 terms of dz leave out at most 2^-18 of it."""
