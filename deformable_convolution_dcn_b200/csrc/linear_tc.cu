@@ -16,9 +16,10 @@
 // an infinity has zeros for its other terms, whose products would make it NaN. The tensor cores cut each step's sum off
 // rather than rounding it, so float32 results take the accumulator out every
 // `chunk` blocks of 64 and add it in registers with proper rounding. bfloat16
-// results leave the whole reduction in the accumulator: cut off they lose 5.8e-5
-// of 12544 positive products, 1.6e-4 of 65536 and 8.6e-4 of 401408 (of products of
-// both signs a quarter of that), their rounding is off by up to 2e-3.
+// results, whose rounding is off by up to 2e-3, do so where the reduction is over 64
+// blocks, in equal pieces of up to 64: left whole, 12544 positive products lost 5.8e-5
+// of their sum, 65536 lost 1.6e-4, 401408 lost 8.6e-4; in pieces they lose 4e-6 at any
+// length (4000x1024x12544 75.4 us, whole 73.7).
 //
 // Warps: 0 and 10 TMA producers of A and B, 1 MMA issue and TMEM, 2-9 epilogue
 // (each of the four TMEM lane quarters twice, once for each half of the columns). Accumulators
@@ -27,7 +28,7 @@
 // 32-byte sectors. Products with too few tiles to fill the GPU are split along
 // the reduction; the parts meet in finish_kernel, in a fixed order.
 //
-// Measured (M x N x K, GPU time): bfloat16 4000x1024x12544 relu 73 us, 1410 TFLOP/s,
+// Measured (M x N x K, GPU time): bfloat16 4000x1024x12544 relu 75 us, 1363 TFLOP/s,
 // the tensor pipe busy 86 % of the cycles, backward 180; 20000x1024x256 18 us, bound by
 // the result's bytes (14.4 where L2 holds x), and 25.5 with relu and a shortcut; backward
 // 20000x256x1024 relu 53 us, 5000x2048x512 gelu 87 us, of which the preparation of dz takes
@@ -57,6 +58,7 @@ constexpr int MAX_SLOTS = 3;
 constexpr uint32_t SMEM_MAX = 227 * 1024, BAR_BYTES = 512;
 constexpr uint32_t SLOT_BYTES = 4096, EXCHANGE_BYTES = 32 * 33 * 4, BIAS_BYTES = 128 * 4;  // a warp
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int LONG = 64;                  // stages that a bfloat16 result's accumulator adds up at most
 constexpr long long WAIT_LIMIT = 2000000000LL;
 
 // How the TMA producer walks an operand (see encode()).
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const OperandDesc da(base, a_mn), db(base + a.a.terms * A_BYTES, b_mn);
             const uint32_t aterm = A_BYTES / 16, bterm = (uint32_t)(a.bn / CG) * 128 / 16;
             const uint32_t stage_units = a.stage_bytes / 16;
-            const bool one = a.a.terms * a.b.terms == 1, two = PB == 0 && a.a.terms * a.b.terms == 2, both = a.b.terms > 1;
+            const bool one = a.a.terms * a.b.terms == 1, two = a.a.terms * a.b.terms == 2, both = a.b.terms > 1;
             const uint32_t a2 = a.a.terms == 2 ? aterm : 0, b2 = aterm == a2 ? 0 : bterm;  // of two: the second product's
             int stage = 0;
             uint32_t phase = 0, acc_phase = 1, off = 0;
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             auto write = [&](float(&v)[COLS], int c) {
                 const int before = emit.out;
-                emit.chunk(v, col + c * COLS, c * COLS, PB != 256 && (PB != 0 || std::is_same<T, bf16>::value));
+                emit.chunk(v, col + c * COLS, c * COLS, std::is_same<T, bf16>::value || (PB != 0 && PB != 256));
                 if (has_res && emit.out != before) {
                     emit.freed();
                     fetch_next();
@@ -615,17 +617,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     write(v, c);
                 }
             } else {
-                float acc[PB / 2] = {};
+                constexpr int HALF = PB / 2 > COLS ? PB / 2 : COLS;
+                float acc[HALF] = {};
                 bool ok = true;
                 for (int c0 = k0; c0 < k1; c0 += a.chunk) {
                     ok = wait_acc();
                     if (!ok) break;
                     const uint32_t from = lanes + buf * 256;
 #pragma unroll
-                    for (int j = 0; j < PB / 2; j += 32) {
+                    for (int j = 0; j < HALF; j += 32) {
+                        if (PB == 64 && HALF == PB && nch == 0) break;
                         float v[32];
                         ptx::tmem_ld32(from + j, v);
-                        if (PB <= 128 && a.a.terms > 1) {
+                        if (std::is_same<T, float>::value && PB <= 128 && a.a.terms > 2) {
                             float l[32];
                             ptx::tmem_ld32(from + 128 + j, l);
 #pragma unroll
@@ -641,7 +645,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < PB / 2; j += 32) write(*reinterpret_cast<float(*)[32]>(&acc[j]), j / 32);
+                for (int j = 0; j < HALF; j += COLS)
+                    if (!(PB == 64 && HALF == PB && nch == 0)) write(*reinterpret_cast<float(*)[COLS]>(&acc[j]), j / COLS);
             }
         }
         // residual chunks asked for have landed, and stores have read their slots, before the CTA leaves (bounded)
@@ -1042,8 +1047,10 @@ GemmPlan plan_gemm(long long rows, long long cols, int red, int ta, int tb, bool
                 }
             }
     }
-    // float32 results: the accumulator is taken out every 256 (terms: 128) elements
-    best.chunk = f32_out ? (prods > 1 ? 2 : 4) : 1 << 28;
+    // float32 results: the accumulator is taken out every 256 (terms: 128) elements; bfloat16 results of reductions over
+    // LONG stages in equal pieces of up to so many
+    const int part = (kblocks + best.splits - 1) / best.splits, pieces = (part + LONG - 1) / LONG;
+    best.chunk = f32_out ? (prods > 1 ? 2 : 4) : pieces > 1 ? (part + pieces - 1) / pieces : 1 << 28;
     return best;
 }
 
@@ -1147,7 +1154,12 @@ cudaError_t run_gemm(const GemmPlan& p, const Matrix& A, bool a_mn, const Matrix
         return p.cg == 2 ? launch_gemm<D, PB, 2>(m, a, grid, smem, st)
                          : launch_gemm<D, PB, 1>(m, a, grid, smem, st);
     };
-    if (f32_out) {
+    const bool taken = !f32_out && p.chunk < a.kblocks;  // out of the accumulator, on the way
+    if (taken && !split) {
+        e = p.bn == 64    ? go(T{}, std::integral_constant<int, 64>{})
+            : p.bn == 128 ? go(T{}, std::integral_constant<int, 128>{})
+                          : go(T{}, std::integral_constant<int, 256>{});
+    } else if (f32_out || taken) {
         e = p.bn == 64    ? go(float{}, std::integral_constant<int, 64>{})
             : p.bn == 128 ? go(float{}, std::integral_constant<int, 128>{})
                           : go(float{}, std::integral_constant<int, 256>{});

@@ -119,3 +119,29 @@ def test_linear_bfloat16_parameter_gradients_by_norm(size, act):
     tol = allowed(M) + (2.0 ** -21 if act in ("silu", "gelu") else 0)
     assert norm_off(gw, product64(dz.t(), d["x"].t())) <= tol
     assert norm_off(gb, dz.sum(0)) <= tol + 2.0 ** -23 * math.sqrt(M) / 8  # (chains of up to a sixteenth of the rows)
+
+
+@pytest.mark.parametrize("size", [(4000, 1024, 12544), (700, 264, 25088), (9, 520, 12544), (300, 72, 65536), (1000, 96, 12545),
+                                  (2000, 40, 6272)], ids=name)
+def test_linear_bfloat16_long_reductions_round_once(size):
+    """Positive products, whose sum cut off at each step drifts down. The accumulator is taken out every 256 steps at
+    most: it loses 256 x 2^-24 / 2 of it (units of 2^-24 to 2^-23, half of one a step, running sums of half the size),
+    7.6e-6, and a value flips to its neighbour where it is within that of the middle: 2^8 to 2^9 of 7.6e-6, 0.4 %, twice
+    that allowed. (The whole of 12544 in the accumulator: 5.8e-5, over 1.5 %.)"""
+    M, N, K = size
+    d = on_gpu(M, N, K, "bf16", 25)
+    x, w = d["x"].abs(), d["w"].abs()
+    y, z = dcn.linear_forward(x, w, activation="silu", need_preact=True)
+    torch.cuda.synchronize()
+    dcn.check_status()
+    want = product64(x, w)
+    assert float((z != want.bfloat16()).double().mean()) <= 0.008
+    r = torch.randn_like(z)  # with the rest of the epilogue
+    y = dcn.linear_forward(x, w, d["b"], r, "relu")
+    want = want + d["b"].double() + r.double()
+    ref.check("y", y, want.clamp(min=0), 2.0 ** -16 * want.abs() + 2.0 ** -8 * want.abs() + 1e-30)
+    # grad_x of as long a reduction
+    gx = dcn.linear_backward(x[:, :N].contiguous(), torch.ones((K, N), dtype=x.dtype, device="cuda"), None, x, "none",
+                             need_weight=False, need_bias=False)[0]
+    want = x.double().sum(1, keepdim=True).expand(M, N)
+    assert float((gx != want.bfloat16()).double().mean()) <= 0.02 and float(((gx.double() - want) / want).abs().max()) <= 1.02 * 2.0 ** -8
